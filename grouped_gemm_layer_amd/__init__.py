@@ -15,7 +15,14 @@ Names follow the C ABI in include/moe.h:
     backward(dims, dy, x, w13, w2, routing, saved, dx, dw13, dw2, dgate, dlogits, ws)
     mxfp8_quantize(src, along, codes, scales)
     mxfp8_quantize_grouped(src, offsets, capacity, pad_off, codes, scales)
-plus allocation helpers (alloc_routing, alloc_workspace) and MoeLayer, a
+    sort_workspace_size(T, k, E); sort_tokens(routing, ws)
+    permute(x, routing, xp, weights); permute_backward(dxp, routing, dx, weights, x, dweights)
+    unpermute(rows, routing, y, weights); unpermute_backward(dy, routing, drows, weights, rows, dweights)
+    mxfp4_quantize(src, codes, scales, along, swiglu); mxfp4_dequantize(codes, scales, out)
+    mxfp4_product(a_codes, a_scales, b_codes, b_scales, c, k, a_format, offsets, row_map, row_div)
+    grad_workspace_size(count); grad_norm(tensors, sumsq, ws); grad_clip(tensors, sumsq, max_norm, norm, out)
+plus GradientList, which owns the buffers of a list of gradients, and
+allocation helpers (alloc_routing, alloc_workspace) and MoeLayer, a
 small holder that owns the buffers of one shape.
 """
 from __future__ import annotations
@@ -28,7 +35,9 @@ __all__ = [
     "MoeError", "lib_path", "load_library", "workspace_size", "route", "forward", "backward",
     "alloc_routing", "alloc_workspace", "status_str", "MoeLayer", "num_kernels", "mxfp8_quantize",
     "mxfp8_quantize_grouped", "mxfp8_grouped_capacity", "route_noalloc", "weight_codes_size", "quantize_weights",
-    "forward_cached", "backward_cached",
+    "forward_cached", "backward_cached", "sort_workspace_size", "sort_tokens", "permute", "permute_backward",
+    "unpermute", "unpermute_backward", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_product", "grad_workspace_size",
+    "grad_norm", "grad_clip", "GradientList",
 ]
 
 MODE_FP32, MODE_BF16, MODE_MXFP8, MODE_FP8_BWD = 0, 1, 2, 3
@@ -55,6 +64,11 @@ class _CRouting(ctypes.Structure):
     _fields_ = [("topk_idx", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("sorted_to_flat", ctypes.c_void_p),
                 ("flat_to_sorted", ctypes.c_void_p)]
+
+
+class _CTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -126,6 +140,22 @@ def load_library():
     lib.moe_mxfp8_grouped_capacity.restype = sz
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
+    i64, f32, psz = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(sz)
+    for f, args in (
+            ("moe_sort_workspace_size", [i32, i32, i32, psz]),
+            ("moe_sort_tokens", [vp, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+            ("moe_permute", [vp, i64, i32, i32, i32, i32, vp, vp, vp, i64, i32, vp]),
+            ("moe_permute_backward", [vp, i64, i32, i32, i32, i32, i32, vp, vp, vp, i64, vp, i64, vp, vp]),
+            ("moe_unpermute", [vp, i64, i32, i32, i32, i32, i32, vp, vp, vp, i64, vp]),
+            ("moe_unpermute_backward", [vp, i64, i32, i32, i32, i32, vp, vp, vp, i64, vp, i64, i32, vp, vp]),
+            ("moe_mxfp4_quantize", [vp, i64, i32, i32, i32, i32, i32, i32, vp, vp, vp]),
+            ("moe_mxfp4_dequantize", [vp, vp, i32, i32, vp, i64, i32, vp]),
+            ("moe_mxfp4_product", [vp, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, i32, vp, i64, i32, i32, vp]),
+            ("moe_grad_workspace_size", [i32, psz]),
+            ("moe_grad_norm", [vp, i32, vp, vp, sz, vp]),
+            ("moe_grad_clip", [vp, i32, vp, f32, vp, vp])):
+        getattr(lib, f).argtypes = args
+        getattr(lib, f).restype = ctypes.c_int
     lib.moe_wgrad_chunk_rows.argtypes = []
     lib.moe_wgrad_chunk_rows.restype = ctypes.c_int32
     _lib = lib
@@ -318,6 +348,317 @@ def mxfp8_quantize_grouped(src, offsets, capacity: int, pad_off, codes, scales, 
     _check(load_library().moe_mxfp8_quantize_grouped(_ptr(src), rows, cols, _ptr(offsets), E, capacity,
                                                      _ptr(pad_off), _ptr(codes), _ptr(scales), _stream(stream)),
            "moe_mxfp8_quantize_grouped")
+
+
+# ---------------------------------------------------------------------------
+# Operators beside the layer
+# ---------------------------------------------------------------------------
+def _type_of(t) -> int:
+    """The moe_type of a tensor's elements."""
+    import torch
+    if t.dtype is torch.bfloat16:
+        return 1
+    if t.dtype is torch.float32:
+        return 0
+    raise ValueError(f"float32 or bfloat16 values expected, got {t.dtype}")
+
+
+def _matrix(t, name):
+    """(rows, cols, row pitch) of a 2-D operand whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: a matrix expected, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap (strides {t.stride()})")
+    return rows, cols, ld
+
+
+def _plain(t, name, dtype, numel=None):
+    """Checks a contiguous tensor of `dtype` (and of `numel` elements)."""
+    if t.dtype is not dtype or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if numel is None else f' of {numel} elements'} "
+                         f"expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def _enqueue(what, stream, tensors, *args):
+    """Calls the library's function `what` on the tensors' device: on `stream`,
+    or on that device's current one.  None of `tensors` may live elsewhere."""
+    import torch
+    lib = load_library()
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"moe_{what}: device tensors expected, got one on {t.device}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"moe_{what}: tensors on {dev} and on {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif dev is not None and stream.device != dev:
+        raise ValueError(f"moe_{what}: a stream of {stream.device} for tensors on {dev}")
+    f = getattr(lib, "moe_" + what)
+    if dev is None or dev.index == torch.cuda.current_device():
+        st = f(*args, stream.cuda_stream)
+    else:   # kernels launch on the current device
+        with torch.cuda.device(dev):
+            st = f(*args, stream.cuda_stream)
+    if st != 0:
+        raise MoeError(st, "moe_" + what)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def sort_workspace_size(T: int, k: int, E: int) -> int:
+    """Bytes of sort_tokens' workspace (moe_sort_workspace_size)."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().moe_sort_workspace_size(T, k, E, ctypes.byref(out)), "moe_sort_workspace_size")
+    return out.value
+
+
+def sort_tokens(routing: RoutingBuffers, ws, stream=None):
+    """Writes routing's counts, offsets and maps from its topk_idx [T, k]
+    (moe_sort_tokens); an index outside [0, E) marks a slot without an expert."""
+    import torch
+    idx = routing.topk_idx
+    if idx.dim() != 2:
+        raise ValueError(f"topk_idx: [T, k] expected, got shape {tuple(idx.shape)}")
+    (T, k), E = idx.shape, routing.counts.numel()
+    _plain(idx, "topk_idx", torch.int32)
+    _plain(routing.counts, "counts", torch.int32)
+    _plain(routing.offsets, "offsets", torch.int32, E + 1)
+    _plain(routing.sorted_to_flat, "sorted_to_flat", torch.int32, T * k)
+    _plain(routing.flat_to_sorted, "flat_to_sorted", torch.int32, T * k)
+    _plain(ws, "ws", torch.uint8)
+    _enqueue("sort_tokens", stream,
+             (idx, routing.counts, routing.offsets, routing.sorted_to_flat, routing.flat_to_sorted, ws),
+             idx.data_ptr(), T, k, E, routing.counts.data_ptr(), routing.offsets.data_ptr(),
+             routing.sorted_to_flat.data_ptr(), routing.flat_to_sorted.data_ptr(), ws.data_ptr(), ws.numel())
+
+
+def _rows_call(tokens, rows, routing, weights, dweights, other, other_like):
+    """Shared checks of the four row calls: (T, H, k, type, row pitches of
+    tokens, rows and other)."""
+    import torch
+    T, H, ldt = _matrix(tokens, "token rows")
+    n, H2, ldr = _matrix(rows, "expert rows")
+    typ = _type_of(tokens)
+    f2s = routing.flat_to_sorted
+    k = routing.topk_idx.shape[1] if T == 0 else f2s.numel() // T
+    _plain(f2s, "flat_to_sorted", torch.int32, T * k)
+    if H != H2 or rows.dtype is not tokens.dtype:
+        raise ValueError(f"token rows {tuple(tokens.shape)} {tokens.dtype} and expert rows {tuple(rows.shape)} "
+                         f"{rows.dtype} do not match")
+    if weights is not None:
+        _plain(weights, "weights", torch.float32, T * k)
+    ldo = 0
+    if dweights is not None:
+        _plain(dweights, "dweights", torch.float32, T * k)
+        if other is None or other.shape != other_like.shape or other.dtype is not tokens.dtype:
+            raise ValueError("dweights needs the forward's rows, of their shape and type")
+        ldo = _matrix(other, "forward rows")[2]
+    return T, H, n, k, typ, ldt, ldr, ldo
+
+
+def permute(x, routing: RoutingBuffers, xp, weights=None, stream=None):
+    """xp[row of slot (t, j)] = weights[t, j] x[t] (moe_permute); rows no slot names stay as they are."""
+    T, H, n, k, typ, ldx, ldp, _ = _rows_call(x, xp, routing, weights, None, None, None)
+    f2s = routing.flat_to_sorted
+    _enqueue("permute", stream, (x, xp, f2s, weights), x.data_ptr(), ldx, T, H, k, typ, f2s.data_ptr(),
+             _addr(weights), xp.data_ptr(), ldp, n)
+
+
+def permute_backward(dxp, routing: RoutingBuffers, dx, weights=None, x=None, dweights=None, stream=None):
+    """dx[t] = sum_j weights[t, j] dxp[row]; dweights[t, j] = <x[t], dxp[row]> (moe_permute_backward)."""
+    T, H, n, k, typ, lddx, ldp, ldx = _rows_call(dx, dxp, routing, weights, dweights, x, dx)
+    f2s = routing.flat_to_sorted
+    other = x if dweights is not None else None
+    _enqueue("permute_backward", stream, (dxp, dx, f2s, weights, other, dweights), dxp.data_ptr(), ldp, n, T, H, k, typ,
+             f2s.data_ptr(), _addr(weights), _addr(other), ldx, dx.data_ptr(), lddx, _addr(dweights))
+
+
+def unpermute(rows, routing: RoutingBuffers, y, weights=None, stream=None):
+    """y[t] = sum_j weights[t, j] rows[row of slot (t, j)] (moe_unpermute)."""
+    T, H, n, k, typ, ldy, ldo, _ = _rows_call(y, rows, routing, weights, None, None, None)
+    f2s = routing.flat_to_sorted
+    _enqueue("unpermute", stream, (rows, y, f2s, weights), rows.data_ptr(), ldo, n, T, H, k, typ, f2s.data_ptr(),
+             _addr(weights), y.data_ptr(), ldy)
+
+
+def unpermute_backward(dy, routing: RoutingBuffers, drows, weights=None, rows=None, dweights=None, stream=None):
+    """drows[row] = weights[t, j] dy[t]; dweights[t, j] = <dy[t], rows[row]> (moe_unpermute_backward)."""
+    T, H, n, k, typ, lddy, lddr, ldo = _rows_call(dy, drows, routing, weights, dweights, rows, drows)
+    f2s = routing.flat_to_sorted
+    other = rows if dweights is not None else None
+    _enqueue("unpermute_backward", stream, (dy, drows, f2s, weights, other, dweights), dy.data_ptr(), lddy, T, H, k, typ,
+             f2s.data_ptr(), _addr(weights), _addr(other), ldo, drows.data_ptr(), lddr, n, _addr(dweights))
+
+
+def mxfp4_quantize(src, codes, scales, along: int = 1, swiglu: bool = False, stream=None):
+    """MXFP4 codes and scales (uint8) of src [rows, cols] or [batch, rows, cols]
+    (moe_mxfp4_quantize): along=1 by rows, codes [.., rows, KB*16] and scales
+    [.., rows, KB]; along=0 transposed, [.., cols, KB*16] and [.., cols, KB].
+    swiglu: src rows are [g1 | g3] and SiLU(g1) * g3 is quantised."""
+    import torch
+    if src.dim() not in (2, 3):
+        raise ValueError(f"src: [rows, cols] or [batch, rows, cols] expected, got shape {tuple(src.shape)}")
+    batch = src.shape[0] if src.dim() == 3 else 1
+    rows, width = src.shape[-2:]
+    ld = src.stride(-2) if rows > 1 else (src.stride(0) if src.dim() == 3 and batch > 1 else width)
+    if (width > 1 and src.stride(-1) != 1) or ld < width or (
+            src.dim() == 3 and batch > 1 and rows > 0 and src.stride(0) != rows * ld):
+        raise ValueError(f"src: contiguous rows at one pitch expected, got strides {src.stride()}")
+    if swiglu and width % 2:
+        raise ValueError(f"src: rows of [g1 | g3] expected, got {width} columns")
+    cols = width // 2 if swiglu else width
+    r, n = (rows, cols) if along else (cols, rows)
+    kb = -(-n // 32)
+    _plain(codes, "codes", torch.uint8, batch * r * kb * 16)
+    _plain(scales, "scales", torch.uint8, batch * r * kb)
+    _enqueue("mxfp4_quantize", stream, (src, codes, scales), src.data_ptr(), ld, batch, rows, cols, _type_of(src), along,
+             int(swiglu), codes.data_ptr(), scales.data_ptr())
+
+
+def mxfp4_dequantize(codes, scales, out, stream=None):
+    """The values of MXFP4 codes and scales as out [.., cols] holds them (moe_mxfp4_dequantize)."""
+    import torch
+    m = out if out.dim() == 2 else out.view(-1, out.shape[-1]) if out.is_contiguous() else None
+    if m is None:
+        raise ValueError("out: a matrix or a contiguous tensor expected")
+    rows, cols, ld = _matrix(m, "out")
+    kb = -(-cols // 32)
+    _plain(codes, "codes", torch.uint8, rows * kb * 16)
+    _plain(scales, "scales", torch.uint8, rows * kb)
+    _enqueue("mxfp4_dequantize", stream, (codes, scales, out), codes.data_ptr(), scales.data_ptr(), rows, cols,
+             m.data_ptr(), ld, _type_of(out))
+
+
+MX_FORMATS = {"mxfp4": 0, "mxfp8": 1}
+
+
+def mxfp4_product(a_codes, a_scales, b_codes, b_scales, c, k: int, a_format: str = "mxfp4", offsets=None, row_map=None,
+                  row_div: int = 1, stream=None):
+    """c[r] = a[row_map[r] // row_div] b[e]^T for rows r of expert e
+    (moe_mxfp4_product).  a: [a_rows, ..] in a_format, b: MXFP4 [E, N, ..] (or
+    [N, ..] without offsets), rows of k values; c: [rows, N] float32 or
+    bfloat16; offsets: int32 [E+1]; row_map: int32 [rows]."""
+    import torch
+    fmt = MX_FORMATS.get(a_format)
+    if fmt is None:
+        raise ValueError(f"a_format: one of {sorted(MX_FORMATS)} expected, got {a_format!r}")
+    rows, N, ldc = _matrix(c, "c")
+    kb = -(-k // 32)
+    E = offsets.numel() - 1 if offsets is not None else 1
+    a_rows = a_codes.shape[0]
+    _plain(a_codes, "a_codes", torch.uint8, a_rows * (kb * 16 if fmt == 0 else k))
+    _plain(a_scales, "a_scales", torch.uint8, a_rows * kb)
+    _plain(b_codes, "b_codes", torch.uint8, E * N * kb * 16)
+    _plain(b_scales, "b_scales", torch.uint8, E * N * kb)
+    if offsets is not None:
+        _plain(offsets, "offsets", torch.int32)
+    if row_map is not None:
+        _plain(row_map, "row_map", torch.int32, rows)
+    elif a_rows < rows:
+        raise ValueError(f"c has {rows} rows, a {a_rows}")
+    _enqueue("mxfp4_product", stream, (a_codes, a_scales, b_codes, b_scales, c, offsets, row_map), a_codes.data_ptr(),
+             a_scales.data_ptr(), a_rows, fmt, b_codes.data_ptr(), b_scales.data_ptr(), E, N, k, _addr(offsets),
+             _addr(row_map), row_div, c.data_ptr(), ldc, rows, _type_of(c))
+
+
+def _tensor_table(tensors, out):
+    """The C array of a list of gradients (and of their outputs)."""
+    if out is not None and len(out) != len(tensors):
+        raise ValueError(f"{len(tensors)} gradients and {len(out)} outputs")
+    table = (_CTensor * max(len(tensors), 1))()
+    for i, t in enumerate(tensors):
+        if not t.is_contiguous():
+            raise ValueError(f"gradient {i}: a contiguous tensor expected, got strides {t.stride()}")
+        c = table[i]
+        c.data, c.n, c.type = t.data_ptr(), t.numel(), _type_of(t)
+        if out is not None:
+            o = out[i]
+            if not o.is_contiguous() or o.dtype is not t.dtype or o.shape != t.shape:
+                raise ValueError(f"output {i}: a contiguous {t.dtype} tensor of shape {tuple(t.shape)} expected")
+            c.out = o.data_ptr()
+    return table
+
+
+def grad_workspace_size(count: int) -> int:
+    """Bytes of grad_norm's workspace for `count` tensors (moe_grad_workspace_size)."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().moe_grad_workspace_size(count, ctypes.byref(out)), "moe_grad_workspace_size")
+    return out.value
+
+
+def _scalar(t, name, dtype):
+    _plain(t, name, dtype, 1)
+
+
+def grad_norm(tensors, sumsq, ws, stream=None):
+    """sumsq (float64, one element) = sum of squares of all tensors (moe_grad_norm)."""
+    import torch
+    _scalar(sumsq, "sumsq", torch.float64)
+    _plain(ws, "ws", torch.uint8)
+    table = _tensor_table(tensors, None)
+    _enqueue("grad_norm", stream, (sumsq, ws, *tensors), ctypes.addressof(table), len(tensors), sumsq.data_ptr(),
+             ws.data_ptr(), ws.numel())
+
+
+def grad_clip(tensors, sumsq, max_norm: float, norm=None, out=None, stream=None):
+    """Scales the tensors by min(1, max_norm / sqrt(sumsq)), in place or into
+    `out`; norm (float32, one element) = sqrt(sumsq) (moe_grad_clip)."""
+    import torch
+    _scalar(sumsq, "sumsq", torch.float64)
+    if norm is not None:
+        _scalar(norm, "norm", torch.float32)
+    table = _tensor_table(tensors, out)
+    _enqueue("grad_clip", stream, (sumsq, norm, *tensors, *(out or ())), ctypes.addressof(table), len(tensors),
+             sumsq.data_ptr(), max_norm, _addr(norm))
+
+
+class GradientList:
+    """The gradients of a step (contiguous float32 or bfloat16 tensors of one
+    device), with the buffers of their norm and the table the library reads.
+    The tensors stay where they are while the list is used; out: where the
+    clipped gradients go (default: in place)."""
+
+    def __init__(self, tensors, out=None):
+        import torch
+        self.tensors = list(tensors)
+        self.out = None if out is None else list(out)
+        if not self.tensors:
+            raise ValueError("at least one gradient expected")
+        dev = self.tensors[0].device
+        self._table = _tensor_table(self.tensors, self.out)
+        self._on_device = (*self.tensors, *(self.out or ()))
+        for t in self._on_device:
+            if t.device != dev:
+                raise ValueError(f"gradients on {dev} and on {t.device}")
+        self.sumsq = torch.empty(1, dtype=torch.float64, device=dev)
+        self.norm = torch.empty((), dtype=torch.float32, device=dev)
+        self.ws = alloc_workspace(grad_workspace_size(len(self.tensors)), dev)
+
+    def sum_squares(self, stream=None):
+        """sumsq (float64 [1]) of these tensors; ranks add theirs up before scale()."""
+        _enqueue("grad_norm", stream, (self.sumsq,), ctypes.addressof(self._table), len(self.tensors),
+                 self.sumsq.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        return self.sumsq
+
+    def scale(self, max_norm: float, stream=None):
+        """Clips by the norm sqrt(sumsq); returns the norm (float32 tensor)."""
+        _enqueue("grad_clip", stream, (self.sumsq,), ctypes.addressof(self._table), len(self.tensors),
+                 self.sumsq.data_ptr(), max_norm, self.norm.data_ptr())
+        return self.norm
+
+    def clip(self, max_norm: float, stream=None):
+        """Norm and clipping in one go; returns the norm (float32 tensor)."""
+        self.sum_squares(stream)
+        return self.scale(max_norm, stream)
 
 
 class MoeLayer:

@@ -252,6 +252,50 @@ hipError_t launch_mx_quant_tokens_t(const T* src, int F, const int32_t* s2f, int
                                     const int32_t* pad_off, int E, int Mp, uint8_t* codes, uint8_t* scales,
                                     hipStream_t s);
 
+// Operators beside the layer (types: 0 fp32, 1 bf16, the public moe_type values)
+// sort by expert (permute.hip); M = T*k slots
+size_t sort_ws_bytes(int64_t M, int E);
+hipError_t launch_sort(const int32_t* idx, int64_t M, int E, int32_t* counts, int32_t* offsets, int32_t* s2f,
+                       int32_t* f2s, int32_t* ws, hipStream_t s);
+// rows between token order and expert order: scatter writes rows_out from
+// token_in, gather writes token_out from rows_in; with dweights the dots of the
+// other operand (rows_in, token_in) are taken too
+struct RowsArgs {
+  int T, H, k, rows;
+  const int32_t* f2s;             // [T*k]
+  const float* weights;           // [T*k] or null
+  float* dweights;                // [T*k] or null
+  const void* token_in;  int64_t ld_token_in;
+  const void* rows_in;   int64_t ld_rows_in;
+  void* token_out;       int64_t ld_token_out;
+  void* rows_out;        int64_t ld_rows_out;
+};
+hipError_t launch_scatter_rows(const RowsArgs& a, int type, hipStream_t s);
+hipError_t launch_gather_rows(const RowsArgs& a, int type, hipStream_t s);
+
+// MXFP4 quantiser and its inverse (mxfp4.hip), layouts as moe_mxfp4_quantize
+hipError_t launch_mx4_quantize(const void* src, int64_t ld, int batch, int rows, int cols, int type, int along,
+                               int swiglu, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out,
+                                 int64_t ld, int type, hipStream_t s);
+// grouped product on MXFP4 weights (gemm_mx4.hip), arguments as moe_mxfp4_product
+struct Mx4Args {
+  const uint8_t *a, *sa;          // [a_rows][pitch_a], [a_rows][KB]
+  const uint8_t *b, *sb;          // [E][N][KB*16], [E][N][KB]
+  const int32_t* offsets;         // [E+1] or null (E = 1, all rows)
+  const int32_t* row_map;         // [rows] or null
+  void* c;
+  int64_t ldc;
+  int a_rows, a_fp8, E, N, K, KB, row_div, rows, c_bf16;
+};
+hipError_t launch_mx4_product(const Mx4Args& a, hipStream_t s);
+// gradient norm and clipping (gradnorm.hip)
+struct GradTensor { const void* data; void* out; int64_t n; int32_t type, reserved; };   // moe_tensor
+size_t grad_ws_bytes(int count);
+hipError_t launch_grad_sumsq(const GradTensor* tensors, int count, double* sumsq, double* ws, hipStream_t s);
+hipError_t launch_grad_clip(const GradTensor* tensors, int count, const double* sumsq, float max_norm,
+                            float* norm_out, hipStream_t s);
+
 // tiling the API layer needs for workspace sizing and the tile table
 int bf16_fwd_row_tile_m();  // token rows per tile of the bf16 forward GEMMs
 bool bf16_dgrad_long(int H, int I);  // the bf16 dgrad GEMMs take their long-K tiles

@@ -349,6 +349,144 @@ size_t moe_mxfp8_grouped_capacity(int32_t rows, int32_t E);
  * build; no GPU needed. */
 int32_t moe_wgrad_chunk_rows(void);
 
+/* ---------------------------------------------------------------------------
+ * Operators beside the layer: rows sorted by expert and back for callers that
+ * run their own experts between routing and combine, the 4-bit microscaled
+ * format with its grouped product, and the gradients' norm and clipping.
+ *
+ * They share the conventions above with these differences: they take their
+ * sizes as arguments instead of moe_dims; data pointers need only the
+ * alignment of their elements (workspaces, codes and scales stay 256-byte
+ * aligned), and 2-D operands have a row pitch `ld` in elements (>= the row
+ * length); offsets are computed in 64 bits, so no operand is limited to 2 GiB
+ * unless stated; a size of zero (no tokens, no rows, no tensors) is valid and
+ * returns MOE_OK.  `type` is a moe_type. */
+typedef enum {
+  MOE_TYPE_FP32 = 0,
+  MOE_TYPE_BF16 = 1
+} moe_type;
+
+/* Tokens sorted by expert, from expert indices the caller has chosen (any
+ * router; TE dropless-MoE page, "01": every token goes to a few experts and
+ * none is dropped).  topk_idx: device [T,k] int32; an index outside [0, E)
+ * marks a slot without an expert here (masked tokens; experts on another GPU).
+ *   counts [E], offsets [E+1]: rows of each expert, exclusive prefix sums
+ *   sorted_to_flat [T*k]: flat slot t*k+j of each row of the stable sort by
+ *     expert; -1 behind the last row offsets[E]
+ *   flat_to_sorted [T*k]: row of each slot, -1 for a slot without an expert
+ * A token may name one expert twice (two rows).  E <= 512.  ws: at least
+ * moe_sort_workspace_size bytes, 256-byte aligned.  Bit-exact, deterministic;
+ * one kernel up to 4096 slots, else two. */
+moe_status moe_sort_workspace_size(int32_t T, int32_t k, int32_t E, size_t* bytes);
+moe_status moe_sort_tokens(const int32_t* topk_idx, int32_t T, int32_t k, int32_t E, int32_t* counts,
+                           int32_t* offsets, int32_t* sorted_to_flat, int32_t* flat_to_sorted, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
+
+/* Rows to the experts and back, with weights, and their gradients (TE
+ * dropless-MoE page, "Optimisation 2": dispatch reorders the tokens' rows,
+ * combine sums the experts' results).  With r = flat_to_sorted[t*k+j] and
+ * w = weights[t,j] (fp32; 1 when weights is NULL), over the slots with
+ * 0 <= r < rows:
+ *   moe_permute:            xp[r] = w x[t]
+ *   moe_permute_backward:   dx[t] = sum_j w dxp[r],   dweights[t,j] = <x[t], dxp[r]>
+ *   moe_unpermute:          y[t]  = sum_j w o[r]
+ *   moe_unpermute_backward: drows[r] = w dy[t],       dweights[t,j] = <dy[t], o[r]>
+ * Other slots add nothing (the sum over none is zero), their dweights are 0,
+ * and rows that no slot names are neither read nor written.  A row must not be
+ * named by two slots in the calls that write rows.  x, y, dx, dy: [T,H]; xp,
+ * dxp, o, drows: [rows,H], all of `type`; weights, dweights: [T,k] fp32.
+ * Products, sums (in slot order) and dots are fp32, outputs rounded once.
+ * dweights may be NULL; x (permute) or o (unpermute) is then not read and may
+ * be NULL.  k <= 32. */
+moe_status moe_permute(const void* x, int64_t ldx, int32_t T, int32_t H, int32_t k, int32_t type,
+                       const int32_t* flat_to_sorted, const float* weights, void* xp, int64_t ldp, int32_t rows,
+                       hipStream_t stream);
+moe_status moe_permute_backward(const void* dxp, int64_t ldp, int32_t rows, int32_t T, int32_t H, int32_t k,
+                                int32_t type, const int32_t* flat_to_sorted, const float* weights, const void* x,
+                                int64_t ldx, void* dx, int64_t lddx, float* dweights, hipStream_t stream);
+moe_status moe_unpermute(const void* o, int64_t ldo, int32_t rows, int32_t T, int32_t H, int32_t k, int32_t type,
+                         const int32_t* flat_to_sorted, const float* weights, void* y, int64_t ldy,
+                         hipStream_t stream);
+moe_status moe_unpermute_backward(const void* dy, int64_t lddy, int32_t T, int32_t H, int32_t k, int32_t type,
+                                  const int32_t* flat_to_sorted, const float* weights, const void* o, int64_t ldo,
+                                  void* drows, int64_t lddr, int32_t rows, float* dweights, hipStream_t stream);
+
+/* MXFP4: the OCP microscaling format with E2M1 elements (0, .5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives), one E8M0 scale per 32 consecutive values, by the
+ * rule of moe_mxfp8_quantize: X = the smallest integer with amax <= 6 * 2^X,
+ * clamped to [-127, 127] (-127 for an all-zero block), scale byte X + 127; codes
+ * = v / 2^X rounded to the nearest value, ties to the even code, sign kept.  A
+ * block that holds an infinity or NaN gets scale byte 255 (NaN) and zero codes.
+ * src: device [batch, rows, cols] of `type`, row pitch ld, matrices `rows` row
+ * pitches apart.
+ *   along = 1: blocks along each row: codes [batch, rows, KB*16], scales
+ *              [batch, rows, KB], KB = ceil(cols / 32)
+ *   along = 0: blocks down each column, written transposed: codes [batch,
+ *              cols, KB*16], scales [batch, cols, KB], KB = ceil(rows / 32)
+ * Value i of a block is in byte i/2, the even one in the low half; a ragged
+ * last block is padded with zeros.  swiglu != 0 (along = 1 only): src rows hold
+ * 2*cols values [g1 | g3] and SiLU(g1) * g3, in fp32, is quantised: the step
+ * between the two expert products.  Deterministic. */
+moe_status moe_mxfp4_quantize(const void* src, int64_t ld, int32_t batch, int32_t rows, int32_t cols, int32_t type,
+                              int32_t along, int32_t swiglu, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+/* out[r, c] = the value of code c of row r (rows * KB scales as above, KB =
+ * ceil(cols / 32)); out: [rows, cols] of `type`, row pitch ld.  Exact: every value
+ * but those of scale 254 (infinite above 1.5 * 2^127) is a bf16 number; scale
+ * 255 gives NaN. */
+moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols, void* out,
+                                int64_t ld, int32_t type, hipStream_t stream);
+
+/* Grouped product on MXFP4 weights (TE dropless-MoE page, "Optimisation 1:
+ * Grouped GEMM", on the 4-bit format):
+ *   c[r] = a[row(r)] b[e]^T      for the rows offsets[e] <= r < offsets[e+1]
+ * a: codes and scales of a_rows rows of K values, a_format MOE_MX_FP4 (as
+ * moe_mxfp4_quantize writes them) or MOE_MX_FP8 (moe_mxfp8_quantize; K a
+ * multiple of 32); b: MXFP4, [E, N, KB*16] and [E, N, KB].  row(r) =
+ * row_map[r] / row_div, or r when row_map is NULL (sorted_to_flat and k gather
+ * token rows; a row outside [0, a_rows) counts as zeros).  offsets: device
+ * int32 [E+1], ascending; NULL with E = 1: all rows.  c: [rows, N] of c_type, row
+ * pitch ldc; rows outside [offsets[0], offsets[E]) are left as they were, and
+ * offsets beyond `rows` are cut off there.  Products of codes are exact and
+ * summed in fp32 (MXFP4 operands; with MXFP8 the matrix cores keep about 1e-4
+ * of a step's sum of magnitudes), rounded once.  A scale of 255 makes every
+ * result it enters NaN.  Deterministic, no workspace.  E <= 512; a_rows times
+ * the bytes of a row, and N times them, below 2 GiB each. */
+typedef enum {
+  MOE_MX_FP4 = 0,
+  MOE_MX_FP8 = 1
+} moe_mx_format;
+moe_status moe_mxfp4_product(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_rows, int32_t a_format,
+                             const uint8_t* b_codes, const uint8_t* b_scales, int32_t E, int32_t N, int32_t K,
+                             const int32_t* offsets, const int32_t* row_map, int32_t row_div, void* c, int64_t ldc,
+                             int32_t rows, int32_t c_type, hipStream_t stream);
+
+/* The global norm of many gradient tensors and clipping by it (the fp32 main
+ * gradients of moe_backward_accumulate, and any others of the step).
+ *   moe_grad_norm: sumsq[0] = sum of squares over all tensors (device fp64: it
+ *     may be added over ranks before the second call); summed in fp64 in a
+ *     fixed order
+ *   moe_grad_clip: norm = sqrt(sumsq[0]); out = grad * min(1, max_norm / norm);
+ *     norm_out[0] = norm (device fp32, or NULL).  A norm that is not finite
+ *     leaves out = grad, for the caller to skip the step.
+ * tensors: host array of `count`, read during the call: `data` device pointer,
+ * `out` the clipped gradient (NULL or equal to data: in place; it must not
+ * overlap anything else), `n` values of `type`.  max_norm >= 0.  Two tensors
+ * that overlap are MOE_ERR_UNSUPPORTED.  ws: at least
+ * moe_grad_workspace_size bytes (host-only), 256-byte aligned; two calls that
+ * run at once need one each. */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t n;
+  int32_t type;
+  int32_t reserved;           /* 0 */
+} moe_tensor;
+moe_status moe_grad_workspace_size(int32_t count, size_t* bytes);
+moe_status moe_grad_norm(const moe_tensor* tensors, int32_t count, double* sumsq, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+moe_status moe_grad_clip(const moe_tensor* tensors, int32_t count, const double* sumsq, float max_norm,
+                         float* norm_out, hipStream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* moe_status_str(moe_status status);
 
