@@ -20,6 +20,13 @@ using gg::make_rsrc;
 using gg::u32x4_t;
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 
+#ifndef MOE_MX4_BIG
+#define MOE_MX4_BIG 256
+#endif
+#ifndef MOE_MX4_MID
+#define MOE_MX4_MID 32
+#endif
+constexpr int MX4_BIG = MOE_MX4_BIG, MX4_MID = MOE_MX4_MID;
 constexpr int KSTEP = 128;   // K of one scaled MFMA
 constexpr int FMT_FP8 = 0, FMT_FP4 = 4;   // format fields of the instruction
 
@@ -28,13 +35,18 @@ constexpr int FMT_FP8 = 0, FMT_FP4 = 4;   // format fields of the instruction
 // experts l*per .. of the offsets, a prefix sum over the lanes and a ballot
 // give the lane that holds tile i.  That takes about 0.5 us of a tile's time
 // and saves the launch that would build a table.  Offsets are cut to [0, rows]
-// so that no index leaves c.  False behind the last tile.
-__device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int i, int lane, int& e, int& m0, int& mlim) {
+// so that no index leaves c.  `pick` gives i from the number of tiles; false
+// when that is no tile.
+template <class Pick>
+__device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int lane, Pick&& pick, int& e, int& m0,
+                                          int& mlim) {
   if (a.offsets == nullptr) {
+    const int total = (a.rows + bm - 1) / bm, i = pick(total);
+    if (i >= total) return false;
     e = 0;
     m0 = i * bm;
     mlim = a.rows;
-    return m0 < mlim;
+    return true;
   }
   const int per = (a.E + 63) / 64;   // <= 8
   int cnt[8], sum = 0;
@@ -56,6 +68,7 @@ __device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int i, int l
     const int v = __shfl_up(inc, off);
     if (lane >= off) inc += v;
   }
+  const int i = pick(__builtin_amdgcn_readlane(inc, 63));
   const uint64_t hit = __ballot(inc > i);
   if (hit == 0) return false;
   const int src = __builtin_ctzll(hit);
@@ -125,7 +138,7 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
   const int g = lane >> 4, rl = lane & 15;
   const int tile = blockIdx.x / n_groups, ng = blockIdx.x % n_groups;
   int e, m0, mlim;
-  if (!find_tile(a, 16 * MF, tile, lane, e, m0, mlim)) return;
+  if (!find_tile(a, 16 * MF, lane, [&](int) { return tile; }, e, m0, mlim)) return;
   const int wk = KS > 1 ? wave : 0, wn = KS > 1 ? 0 : wave;
   const int n0 = (ng * NWV + wn) * 16;
   const uint32_t pb = (uint32_t)a.KB * 16, pa = FP8 ? (uint32_t)a.K : pb;   // code bytes of a row
@@ -219,6 +232,261 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows per expert: BM x BN tiles, operands through LDS.
+//
+// K advances by stages of KST (256 with MXFP4 rows, 128 with MXFP8: either way
+// 128 bytes, a whole line, per row of A).  Two stages of LDS: while one is
+// multiplied, the other receives the next by buffer-to-LDS DMA (16 bytes a
+// lane; lanes outside a row, its K or the tile read zeros through an
+// out-of-range offset).  One barrier per stage.  Code rows are cut in 16-byte
+// chunks, XOR-swizzled within 128 bytes, so that a fragment's 64 chunks cover
+// every bank equally; with MXFP8 rows, B's 64-byte rows lie in pairs.
+//
+// Scales: thread t owns row t of the stage's BM + BN rows, loads its 8 (4)
+// bytes of the next stage into a register and, after the products, writes them
+// to LDS in the order the lanes consume them: lane (r, g) of wave row w finds
+// the bytes of its FM row blocks and both K steps side by side, so one LDS read
+// per operand and stage brings them all, and the instruction's byte select
+// picks each one.
+// ---------------------------------------------------------------------------
+template <int N, class F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl<N>(f, std::make_integer_sequence<int, N>{});
+}
+
+template <bool FP8_, int BM_, int BN_, int WGM_, int WGN_>
+struct Mx4Cfg {
+  static constexpr bool FP8 = FP8_;
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
+  static constexpr int NW = WGM * WGN, NTHR = 64 * NW;
+  static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
+  static constexpr int KST = FP8 ? 128 : 256;            // K per stage
+  static constexpr int SS = KST / KSTEP;                 // MFMA steps per stage
+  static constexpr int RA = 128, RB = KST / 2;           // code bytes per row and stage
+  static constexpr int SB = KST / 32;                    // scale bytes per row and stage
+  static constexpr int A_BYTES = BM * RA, B_BYTES = BN * RB;
+  static constexpr int DA = A_BYTES / 1024 / NW, DB = B_BYTES / 1024 / NW;   // 1 KiB DMAs per wave
+  static constexpr int A_SC = A_BYTES + B_BYTES, B_SC = A_SC + BM * SB;
+  static constexpr int STAGE = B_SC + BN * SB;
+  static constexpr int LDS = 2 * STAGE;
+  static_assert(DA * NW * 1024 == A_BYTES && DB * NW * 1024 == B_BYTES, "whole DMAs per wave");
+  static_assert(BM + BN == NTHR, "one scale row per thread");
+  static_assert(FM * SS % 4 == 0 && FN * SS % 4 == 0, "whole words of scales per lane");
+};
+
+template <class C>
+__global__ __launch_bounds__(C::NTHR) void mx4_tile_kernel(Mx4Args a, int n_tiles) {
+  constexpr int BM = C::BM, BN = C::BN, WM = C::WM, WN = C::WN, FM = C::FM, FN = C::FN, NW = C::NW, SS = C::SS;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WGN, wn = wave % C::WGN;
+  const int g = lane >> 4, rl = lane & 15;
+  // block b runs on XCD b % 8; each XCD takes a contiguous run of the tiles, column tiles fastest, so that
+  // the tiles sharing an expert's rows and weights meet in one L2
+  int e, m0, mlim, nt;
+  const bool live = find_tile(a, BM, lane, [&](int total) {
+    const int64_t tiles = (int64_t)total * n_tiles;
+    const int per_xcd = (int)((tiles + gg::NXCD - 1) / gg::NXCD);
+    const int x = blockIdx.x % gg::NXCD, j = blockIdx.x / gg::NXCD;
+    const int64_t L = (int64_t)x * per_xcd + j;
+    if (j >= per_xcd || L >= tiles) return INT32_MAX;
+    nt = (int)(L % n_tiles);
+    return (int)(L / n_tiles);
+  }, e, m0, mlim);
+  if (!live) return;
+  const int n0 = nt * BN;
+
+  const uint32_t pb = (uint32_t)a.KB * 16, pa = C::FP8 ? (uint32_t)a.K : pb;   // code bytes of a row
+  const auto rb = make_rsrc(a.b + (size_t)e * a.N * pb, (uint32_t)a.N * pb);
+  const auto ra = make_rsrc(a.a, (uint32_t)a.a_rows * pa);
+  const int nk = (a.K + C::KST - 1) / C::KST;
+
+  // DMA i of wave w fills the 1 KiB block ci = i * NW + w of an operand: lane l
+  // writes 16 bytes at 16 l, which hold chunk `col` of row `row` of that block
+  const int line = lane >> 3, phys = lane & 7, chunk8 = phys ^ line;
+  const uint32_t cola = 16u * chunk8;                                          // 8 rows of 128 bytes
+  const uint32_t colb = C::RB == 128 ? 16u * chunk8 : 16u * (chunk8 & 3);      // or 16 rows of 64
+  uint32_t oa[C::DA], ob[C::DB];
+#pragma unroll
+  for (int i = 0; i < C::DA; ++i) {
+    const int m = m0 + 8 * (i * NW + wave) + line;
+    const int s = m < mlim ? a_row(a, m) : -1;
+    oa[i] = s >= 0 ? (uint32_t)s * pa + cola : OOB;
+  }
+#pragma unroll
+  for (int i = 0; i < C::DB; ++i) {
+    const int ci = i * NW + wave;
+    const int n = n0 + (C::RB == 128 ? 8 * ci + line : 16 * ci + 2 * line + (chunk8 >> 2));
+    ob[i] = n < a.N ? (uint32_t)n * pb + colb : OOB;
+  }
+  const uint32_t lds0 = (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)smem;
+  auto issue = [&](int kt, int st) __attribute__((always_inline)) {
+    const uint32_t base = lds0 + (uint32_t)(st * C::STAGE);
+    const uint32_t ka = (uint32_t)kt * C::RA, kb = (uint32_t)kt * C::RB;
+    const bool in_a = cola + ka < pa, in_b = colb + kb < pb;
+#pragma unroll
+    for (int i = 0; i < C::DA; ++i)
+      gg::dma16(ra, in_a ? oa[i] + ka : OOB, __builtin_amdgcn_readfirstlane(base + (i * NW + wave) * 1024));
+#pragma unroll
+    for (int i = 0; i < C::DB; ++i)
+      gg::dma16(rb, in_b ? ob[i] + kb : OOB, __builtin_amdgcn_readfirstlane(base + C::A_BYTES + (i * NW + wave) * 1024));
+  };
+
+  // this thread's scale row: source, and where its bytes go (stage-relative)
+  using sc_t = std::conditional_t<C::SB == 8, uint64_t, uint32_t>;
+  typedef sc_t scu_t __attribute__((aligned(1)));
+  const bool sc_b = tid >= BM;
+  const int R = sc_b ? tid - BM : tid;
+  int64_t sc_row = -1, sc_end;
+  const uint8_t* sc_base;
+  if (sc_b) {
+    if (n0 + R < a.N) sc_row = ((int64_t)e * a.N + n0 + R) * a.KB;
+    sc_base = a.sb;
+    sc_end = (int64_t)a.E * a.N * a.KB;
+  } else {
+    const int s = m0 + R < mlim ? a_row(a, m0 + R) : -1;
+    if (s >= 0) sc_row = (int64_t)s * a.KB;
+    sc_base = a.sa;
+    sc_end = (int64_t)a.a_rows * a.KB;
+  }
+  const int WX = sc_b ? WN : WM, FX = sc_b ? FN : FM;
+  const int sc_dst = (sc_b ? C::B_SC : C::A_SC) + (((R / WX) * 16 + R % 16) * 4) * (FX * SS) + ((R % WX) / 16) * SS;
+  // SB scale bytes of stage kt; those past the row's end zero.  The last bytes of the array are read from SB
+  // before its end and shifted down.
+  auto load_scales = [&](int kt) __attribute__((always_inline)) -> sc_t {
+    sc_t v = 0;
+    const int rem = a.KB - kt * C::SB;
+    if (sc_row >= 0) {
+      const int64_t at = sc_row + (int64_t)kt * C::SB, lim = sc_end - C::SB;
+      const int64_t from = at < lim ? at : lim;
+      v = *reinterpret_cast<const scu_t*>(sc_base + from) >> (8 * (int)(at - from));
+    }
+    if (rem < C::SB) v &= ((sc_t)1 << (8 * rem)) - 1;
+    return v;
+  };
+  auto store_scales = [&](sc_t v, int st) __attribute__((always_inline)) {
+    uint8_t* p = smem + st * C::STAGE + sc_dst;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {   // K block q of the step(s): the lanes with g = q
+      if constexpr (SS == 2)
+        *reinterpret_cast<uint16_t*>(p + q * (FX * SS)) = (uint16_t)(((v >> (8 * q)) & 0xFF) | ((v >> (32 + 8 * q)) & 0xFF) << 8);
+      else
+        p[q * FX] = (uint8_t)(v >> (8 * q));
+    }
+  };
+
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const bool idle = m0 + wm * WM >= mlim;   // no row of this wave: it only moves data
+
+  auto multiply = [&](int st) __attribute__((always_inline)) {
+    const uint8_t* base = smem + st * C::STAGE;
+    constexpr int WA = FM * SS / 4, WB = FN * SS / 4;   // words of scales
+    uint32_t xa[WA], xb[WB];
+    const uint32_t* pxa = reinterpret_cast<const uint32_t*>(base + C::A_SC + ((wm * 16 + rl) * 4 + g) * (FM * SS));
+    const uint32_t* pxb = reinterpret_cast<const uint32_t*>(base + C::B_SC + ((wn * 16 + rl) * 4 + g) * (FN * SS));
+#pragma unroll
+    for (int w = 0; w < WA; ++w) xa[w] = pxa[w];
+#pragma unroll
+    for (int w = 0; w < WB; ++w) xb[w] = pxb[w];
+    static_for<SS>([&](auto s_) {
+      constexpr int s = s_;
+      i32x8_t fa[FM], fb[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int row = wn * WN + 16 * j + rl;
+        int off;
+        if constexpr (C::RB == 128) off = row * 128 + (((4 * s + g) ^ (row & 7)) << 4);
+        else off = (row >> 1) * 128 + ((((row & 1) * 4 + g) ^ ((row >> 1) & 7)) << 4);
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(base + C::A_BYTES + off);
+        fb[j] = i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int row = wm * WM + 16 * i + rl;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(base + row * 128 + (((C::FP8 ? g : 4 * s + g) ^ (row & 7)) << 4));
+        u32x4_t h = {0u, 0u, 0u, 0u};
+        if constexpr (C::FP8) h = *reinterpret_cast<const u32x4_t*>(base + row * 128 + (((4 + g) ^ (row & 7)) << 4));
+        fa[i] = i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+      }
+      static_for<FM>([&](auto i_) {
+        static_for<FN>([&](auto j_) {
+          constexpr int i = i_, j = j_, ia = i * SS + s, ib = j * SS + s;
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fb[j], fa[i], acc[i][j], FMT_FP4, C::FP8 ? FMT_FP8 : FMT_FP4, ib % 4, (int)xb[ib / 4], ia % 4,
+              (int)xa[ia / 4]);
+        });
+      });
+    });
+  };
+
+  sc_t sc = load_scales(0);
+  issue(0, 0);
+  gg::vm_wait<0>();
+  store_scales(sc, 0);
+  __syncthreads();
+  for (int kt = 0; kt < nk; ++kt) {
+    const int st = kt & 1;
+    if (kt + 1 < nk) {
+      sc = load_scales(kt + 1);
+      issue(kt + 1, st ^ 1);
+    }
+    if (!idle) multiply(st);
+    gg::vm_wait<0>();
+    if (kt + 1 < nk) store_scales(sc, st ^ 1);
+    __syncthreads();
+  }
+
+  // the tile leaves through LDS, CH rows at a time, so that the stores run along its rows
+  auto copy_out = [&](auto zero) __attribute__((always_inline)) {
+    using T = decltype(zero);
+    constexpr int VT = 16 / (int)sizeof(T);                 // values per 16-byte piece
+    constexpr int NQ = BN / VT, ROWB = BN * (int)sizeof(T);
+    constexpr int CH = BM * ROWB <= C::LDS ? BM : BM * ROWB <= 2 * C::LDS ? BM / 2 : BM / 4;
+    static_assert(CH * ROWB <= C::LDS && CH % 16 == 0, "row chunk fits");
+#pragma unroll
+    for (int ch = 0; ch < BM / CH; ++ch) {
+      if (ch > 0) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if ((wm * WM + 16 * i) / CH != ch) continue;        // a 16-row block lies in one chunk
+        const int row = (wm * WM + 16 * i) % CH + rl;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int byte = (wn * WN + 16 * j + 4 * g) * (int)sizeof(T);
+          uint8_t* p = smem + row * ROWB + (((byte >> 4) ^ (row % NQ)) << 4) + (byte & 15);
+          const f32x4_t v = acc[i][j];
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(p) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+          else
+            *reinterpret_cast<f32x4_t*>(p) = v;
+        }
+      }
+      __syncthreads();
+      T* c = static_cast<T*>(a.c);
+      for (int q0 = tid; q0 < CH * NQ; q0 += C::NTHR) {
+        const int row = q0 / NQ, q = q0 % NQ;
+        const int m = m0 + ch * CH + row, n = n0 + q * VT;
+        const int cnt = min(VT, a.N - n);
+        if (m < mlim && cnt > 0) {
+          const RowVec<T> v = {*reinterpret_cast<const u32x4v_t*>(smem + row * ROWB + ((q ^ (row % NQ)) << 4))};
+          v.store(c + (int64_t)m * a.ldc + n, cnt);
+        }
+      }
+    }
+  };
+  if (a.c_bf16) copy_out(bf16_t{});
+  else copy_out(float{});
+}
+
 // row tiles of height bm at most: every expert with rows ends in a partial one
 int64_t max_tiles(const Mx4Args& a, int bm) {
   if (a.offsets == nullptr) return ((int64_t)a.rows + bm - 1) / bm;
@@ -234,8 +502,21 @@ hipError_t launch_stream(const Mx4Args& a, hipStream_t s) {
   return launch_kernel(mx4_stream_kernel<FP8, SC4, MF, KS>, dim3((unsigned)grid), dim3(256), 0, s, a, n_groups);
 }
 
+template <class C>
+hipError_t launch_tiles(const Mx4Args& a, hipStream_t s) {
+  const int n_tiles = (a.N + C::BN - 1) / C::BN;
+  const int64_t tiles = max_tiles(a, C::BM) * n_tiles;
+  const int64_t grid = (tiles + gg::NXCD - 1) / gg::NXCD * gg::NXCD;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  return launch_kernel(mx4_tile_kernel<C>, dim3((unsigned)grid), dim3(C::NTHR), 0, s, a, n_tiles);
+}
+
 template <bool FP8, bool SC4>
 hipError_t launch_formats(const Mx4Args& a, hipStream_t s) {
+  // the tile kernel reads scales 8 bytes at a time and needs that many in each array
+  const bool room = (int64_t)a.a_rows * a.KB >= 8 && (int64_t)a.E * a.N * a.KB >= 8;
+  if (room && a.rows / a.E >= MX4_BIG) return launch_tiles<Mx4Cfg<FP8, 256, 256, 2, 4>>(a, s);
+  if (room && a.rows / a.E >= MX4_MID) return launch_tiles<Mx4Cfg<FP8, 128, 128, 2, 2>>(a, s);
   return launch_stream<FP8, SC4, 1, 4>(a, s);
 }
 
