@@ -49,7 +49,10 @@ struct RowVecBase {
 #pragma unroll
     for (int i = 0; i < N - 1; ++i)
       if (i < n) {
-        if constexpr (sizeof(T) == 4) p[i] = __builtin_bit_cast(T, v[i]);
+        if constexpr (sizeof(T) == 4) {
+          const uint32_t w = v[i];   // a value of its own: a bit cast of the vector's element takes element 0
+          p[i] = __builtin_bit_cast(T, w);
+        }
         else p[i] = (T)(v[i / 2] >> (16 * (i % 2)));
       }
   }

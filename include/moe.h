@@ -430,9 +430,9 @@ moe_status moe_unpermute_backward(const void* dy, int64_t lddy, int32_t T, int32
 moe_status moe_mxfp4_quantize(const void* src, int64_t ld, int32_t batch, int32_t rows, int32_t cols, int32_t type,
                               int32_t along, int32_t swiglu, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 /* out[r, c] = the value of code c of row r (rows * KB scales as above, KB =
- * ceil(cols / 32)); out: [rows, cols] of `type`, row pitch ld.  Exact: every value
- * but those of scale 254 (infinite above 1.5 * 2^127) is a bf16 number; scale
- * 255 gives NaN. */
+ * ceil(cols / 32)); out: [rows, cols] of `type`, row pitch ld.  Exact: the values
+ * are bf16 numbers, but for those of 2^128 and more (codes 4 and 6 of scale
+ * byte 253, from 2 of byte 254), which become infinite; byte 255 gives NaN. */
 moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols, void* out,
                                 int64_t ld, int32_t type, hipStream_t stream);
 
