@@ -383,29 +383,33 @@ def _plain(t, name, dtype, numel=None):
 
 def _enqueue(what, stream, tensors, *args):
     """Calls the library's function `what` on the tensors' device: on `stream`,
-    or on that device's current one.  None of `tensors` may live elsewhere."""
+    or on that device's current one.  None of `tensors` may live elsewhere.
+    (Plain device numbers and the raw stream: the torch.device and Stream
+    objects cost 2 us more, a third of a small call.)"""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     dev = None
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"moe_{what}: device tensors expected, got one on {t.device}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"moe_{what}: tensors on {dev} and on {t.device}")
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError(f"moe_{what}: device tensors expected, got one on {t.device}")
+                if dev is not None:
+                    raise ValueError(f"moe_{what}: tensors on devices {dev} and {d}")
+                dev = d
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif dev is not None and stream.device != dev:
-        raise ValueError(f"moe_{what}: a stream of {stream.device} for tensors on {dev}")
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"moe_{what}: a stream of {stream.device} for tensors on device {dev}")
+        raw = stream.cuda_stream
     f = getattr(lib, "moe_" + what)
-    if dev is None or dev.index == torch.cuda.current_device():
-        st = f(*args, stream.cuda_stream)
+    if dev == torch.cuda.current_device():
+        st = f(*args, raw)
     else:   # kernels launch on the current device
         with torch.cuda.device(dev):
-            st = f(*args, stream.cuda_stream)
+            st = f(*args, raw)
     if st != 0:
         raise MoeError(st, "moe_" + what)
 
@@ -571,20 +575,28 @@ def mxfp4_product(a_codes, a_scales, b_codes, b_scales, c, k: int, a_format: str
 
 
 def _tensor_table(tensors, out):
-    """The C array of a list of gradients (and of their outputs)."""
-    if out is not None and len(out) != len(tensors):
-        raise ValueError(f"{len(tensors)} gradients and {len(out)} outputs")
-    table = (_CTensor * max(len(tensors), 1))()
-    for i, t in enumerate(tensors):
-        if not t.is_contiguous():
-            raise ValueError(f"gradient {i}: a contiguous tensor expected, got strides {t.stride()}")
-        c = table[i]
-        c.data, c.n, c.type = t.data_ptr(), t.numel(), _type_of(t)
-        if out is not None:
-            o = out[i]
-            if not o.is_contiguous() or o.dtype is not t.dtype or o.shape != t.shape:
-                raise ValueError(f"output {i}: a contiguous {t.dtype} tensor of shape {tuple(t.shape)} expected")
-            c.out = o.data_ptr()
+    """The C array (moe_tensor) of a list of gradients and of their outputs: four
+    64-bit words each, the type in the low half of the last."""
+    import array
+    for name, ts in (("gradient", tensors), ("output", out or ())):
+        if not all([t.is_contiguous() for t in ts]):
+            i = [t.is_contiguous() for t in ts].index(False)
+            raise ValueError(f"{name} {i}: a contiguous tensor expected, got strides {ts[i].stride()}")
+    n = [t.numel() for t in tensors]
+    kinds = [t.dtype for t in tensors]
+    code = {dt: _type_of(tensors[kinds.index(dt)]) for dt in set(kinds)}
+    table = array.array("q", bytes(32 * max(len(tensors), 1)))
+    if tensors:
+        table[0::4] = array.array("q", [t.data_ptr() for t in tensors])
+        table[2::4] = array.array("q", n)
+        table[3::4] = array.array("q", [code[dt] for dt in kinds])
+    if out is not None:
+        if len(out) != len(tensors):
+            raise ValueError(f"{len(tensors)} gradients and {len(out)} outputs")
+        if [t.numel() for t in out] != n or [t.dtype for t in out] != kinds:
+            raise ValueError("every output needs its gradient's size and type")
+        if out:
+            table[1::4] = array.array("q", [t.data_ptr() for t in out])
     return table
 
 
@@ -605,7 +617,7 @@ def grad_norm(tensors, sumsq, ws, stream=None):
     _scalar(sumsq, "sumsq", torch.float64)
     _plain(ws, "ws", torch.uint8)
     table = _tensor_table(tensors, None)
-    _enqueue("grad_norm", stream, (sumsq, ws, *tensors), ctypes.addressof(table), len(tensors), sumsq.data_ptr(),
+    _enqueue("grad_norm", stream, (sumsq, ws, *tensors), table.buffer_info()[0], len(tensors), sumsq.data_ptr(),
              ws.data_ptr(), ws.numel())
 
 
@@ -617,7 +629,7 @@ def grad_clip(tensors, sumsq, max_norm: float, norm=None, out=None, stream=None)
     if norm is not None:
         _scalar(norm, "norm", torch.float32)
     table = _tensor_table(tensors, out)
-    _enqueue("grad_clip", stream, (sumsq, norm, *tensors, *(out or ())), ctypes.addressof(table), len(tensors),
+    _enqueue("grad_clip", stream, (sumsq, norm, *tensors, *(out or ())), table.buffer_info()[0], len(tensors),
              sumsq.data_ptr(), max_norm, _addr(norm))
 
 
@@ -635,23 +647,22 @@ class GradientList:
             raise ValueError("at least one gradient expected")
         dev = self.tensors[0].device
         self._table = _tensor_table(self.tensors, self.out)
-        self._on_device = (*self.tensors, *(self.out or ()))
-        for t in self._on_device:
-            if t.device != dev:
-                raise ValueError(f"gradients on {dev} and on {t.device}")
+        at = {t.get_device() for t in (*self.tensors, *(self.out or ()))}
+        if len(at) > 1 or min(at) < 0:
+            raise ValueError(f"gradients and outputs on one GPU expected, got devices {sorted(at)}")
         self.sumsq = torch.empty(1, dtype=torch.float64, device=dev)
         self.norm = torch.empty((), dtype=torch.float32, device=dev)
         self.ws = alloc_workspace(grad_workspace_size(len(self.tensors)), dev)
 
     def sum_squares(self, stream=None):
         """sumsq (float64 [1]) of these tensors; ranks add theirs up before scale()."""
-        _enqueue("grad_norm", stream, (self.sumsq,), ctypes.addressof(self._table), len(self.tensors),
+        _enqueue("grad_norm", stream, (self.sumsq,), self._table.buffer_info()[0], len(self.tensors),
                  self.sumsq.data_ptr(), self.ws.data_ptr(), self.ws.numel())
         return self.sumsq
 
     def scale(self, max_norm: float, stream=None):
         """Clips by the norm sqrt(sumsq); returns the norm (float32 tensor)."""
-        _enqueue("grad_clip", stream, (self.sumsq,), ctypes.addressof(self._table), len(self.tensors),
+        _enqueue("grad_clip", stream, (self.sumsq,), self._table.buffer_info()[0], len(self.tensors),
                  self.sumsq.data_ptr(), max_norm, self.norm.data_ptr())
         return self.norm
 

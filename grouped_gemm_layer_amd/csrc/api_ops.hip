@@ -184,14 +184,14 @@ static_assert(sizeof(moe_tensor) == sizeof(GradTensor) && offsetof(moe_tensor, o
               "the kernels' view of moe_tensor");
 
 // `written`: the call writes `out` (in place where it is NULL or data), so no
-// byte of an output may belong to another tensor or to another tensor's
-// gradient; without it the gradients are only read.
+// byte of an output may belong to another output or to another gradient, and
+// no gradient may be there twice; without it the gradients are only read.
 moe_status check_tensors(const moe_tensor* t, int32_t count, bool written) {
   if (count < 0) return MOE_ERR_DIMS;
   if (count > 0 && !t) return MOE_ERR_NULL;
   int64_t total = 0;
   for (int32_t i = 0; i < count; ++i) {
-    if (t[i].n < 0 || t[i].n > ((int64_t)1 << 44)) return MOE_ERR_DIMS;
+    if (t[i].n < 0 || t[i].n > ((int64_t)1 << 40)) return MOE_ERR_DIMS;
     total += t[i].n;
     if (!type_ok(t[i].type)) return MOE_ERR_UNSUPPORTED;
     if (t[i].n == 0) continue;
@@ -199,7 +199,8 @@ moe_status check_tensors(const moe_tensor* t, int32_t count, bool written) {
     if (!aligned_to(t[i].data, type_size(t[i].type)) || !aligned_to(t[i].out, type_size(t[i].type)))
       return MOE_ERR_ALIGN;
   }
-  if (total > ((int64_t)1 << 45)) return MOE_ERR_DIMS;
+  if (total > ((int64_t)1 << 40)) return MOE_ERR_DIMS;   // (the kernels count chunks of them in 32 bits)
+  if (!written) return MOE_OK;
   // byte ranges of the gradients, and of outputs elsewhere: no two may overlap
   struct Range { uintptr_t lo, hi; };
   try {
@@ -210,7 +211,7 @@ moe_status check_tensors(const moe_tensor* t, int32_t count, bool written) {
       if (bytes == 0) continue;
       const uintptr_t d = reinterpret_cast<uintptr_t>(t[i].data), o = reinterpret_cast<uintptr_t>(t[i].out);
       r.push_back({d, d + bytes});
-      if (written && o && o != d) r.push_back({o, o + bytes});
+      if (o && o != d) r.push_back({o, o + bytes});
     }
     auto less = [](const Range& a, const Range& b) { return a.lo < b.lo; };
     if (!std::is_sorted(r.begin(), r.end(), less)) std::sort(r.begin(), r.end(), less);

@@ -14,22 +14,21 @@
 namespace moe {
 namespace {
 
-constexpr int TENSORS_PER_LAUNCH = 96;      // 3.1 KB of kernel arguments
+constexpr int TENSORS_PER_LAUNCH = 128;     // 3.6 KB of kernel arguments
 constexpr int GRAD_CHUNK = 16384;           // values per chunk
 constexpr int GRAD_BLOCKS = 2048;           // thread blocks of a launch at most: 8 per compute unit
 
 struct TensorTable {
   const void* data[TENSORS_PER_LAUNCH];
   void* out[TENSORS_PER_LAUNCH];
-  int64_t n[TENSORS_PER_LAUNCH];
-  int64_t chunk0[TENSORS_PER_LAUNCH];       // first chunk of the tensor
-  uint8_t bf16[TENSORS_PER_LAUNCH];
+  int64_t n[TENSORS_PER_LAUNCH];            // values; ~values for a bf16 tensor
+  uint32_t chunk0[TENSORS_PER_LAUNCH];      // first chunk of the tensor
   int count;
-  int64_t chunks;
+  uint32_t chunks;                          // the host checks that all values give fewer than 2^31
 };
-static_assert(sizeof(TensorTable) <= 3584, "kernel arguments stay below 4 KB");
+static_assert(sizeof(TensorTable) <= 3800, "kernel arguments stay below 4 KB");
 
-__device__ __forceinline__ int find_tensor(const TensorTable& t, int64_t chunk) {   // uniform over the block
+__device__ __forceinline__ int find_tensor(const TensorTable& t, uint32_t chunk) {   // uniform over the block
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -75,11 +74,13 @@ __device__ __forceinline__ double block_sum(double v, double* s_w) {
 __global__ __launch_bounds__(256) void grad_sumsq_kernel(TensorTable t, double* __restrict__ partials) {
   __shared__ double s_w[4];
   double s = 0.0;
-  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int k = find_tensor(t, c);
-    const int64_t i0 = (c - t.chunk0[k]) * GRAD_CHUNK, n = min((int64_t)GRAD_CHUNK, t.n[k] - i0);
-    s += t.bf16[k] ? chunk_sumsq(static_cast<const bf16_t*>(t.data[k]) + i0, n)
-                   : chunk_sumsq(static_cast<const float*>(t.data[k]) + i0, n);
+    const bool bf16 = t.n[k] < 0;
+    const int64_t i0 = (int64_t)(c - t.chunk0[k]) * GRAD_CHUNK;
+    const int64_t n = min((int64_t)GRAD_CHUNK, (bf16 ? ~t.n[k] : t.n[k]) - i0);
+    s += bf16 ? chunk_sumsq(static_cast<const bf16_t*>(t.data[k]) + i0, n)
+              : chunk_sumsq(static_cast<const float*>(t.data[k]) + i0, n);
   }
   s = block_sum(s, s_w);
   if (threadIdx.x == 0) partials[blockIdx.x] = s;
@@ -128,11 +129,13 @@ __global__ __launch_bounds__(256) void grad_clip_kernel(TensorTable t, const dou
   const bool scale = norm > (double)max_norm && norm <= 1.7976931348623157e308;   // a norm that is not finite clips nothing
   const float f = scale ? (float)((double)max_norm / norm) : 1.f;
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int k = find_tensor(t, c);
     if (!scale && t.out[k] == t.data[k]) continue;
-    const int64_t i0 = (c - t.chunk0[k]) * GRAD_CHUNK, n = min((int64_t)GRAD_CHUNK, t.n[k] - i0);
-    if (t.bf16[k])
+    const bool bf16 = t.n[k] < 0;
+    const int64_t i0 = (int64_t)(c - t.chunk0[k]) * GRAD_CHUNK;
+    const int64_t n = min((int64_t)GRAD_CHUNK, (bf16 ? ~t.n[k] : t.n[k]) - i0);
+    if (bf16)
       chunk_scale(static_cast<const bf16_t*>(t.data[k]) + i0, static_cast<bf16_t*>(t.out[k]) + i0, n, f, scale);
     else
       chunk_scale(static_cast<const float*>(t.data[k]) + i0, static_cast<float*>(t.out[k]) + i0, n, f, scale);
@@ -148,10 +151,9 @@ TensorTable next_table(const GradTensor* tensors, int count, int& at) {
     const int k = t.count++;
     t.data[k] = g.data;
     t.out[k] = g.out ? g.out : const_cast<void*>(g.data);
-    t.n[k] = g.n;
+    t.n[k] = g.type == 1 ? ~g.n : g.n;
     t.chunk0[k] = t.chunks;
-    t.bf16[k] = g.type == 1;
-    t.chunks += (g.n + GRAD_CHUNK - 1) / GRAD_CHUNK;
+    t.chunks += (uint32_t)((g.n + GRAD_CHUNK - 1) / GRAD_CHUNK);
   }
   return t;
 }

@@ -470,8 +470,8 @@ moe_status moe_mxfp4_product(const uint8_t* a_codes, const uint8_t* a_scales, in
  *     leaves out = grad, for the caller to skip the step.
  * tensors: host array of `count`, read during the call: `data` device pointer,
  * `out` the clipped gradient (NULL or equal to data: in place; it must not
- * overlap anything else), `n` values of `type`.  max_norm >= 0.  Two tensors
- * that overlap are MOE_ERR_UNSUPPORTED.  ws: at least
+ * overlap anything else), `n` values of `type`, 2^40 in all at most.  max_norm
+ * >= 0.  moe_grad_clip refuses tensors that overlap (MOE_ERR_UNSUPPORTED).  ws: at least
  * moe_grad_workspace_size bytes (host-only), 256-byte aligned; two calls that
  * run at once need one each. */
 typedef struct {

@@ -131,8 +131,9 @@ def test_gradients():
         assert f([(None, None, 5, 0)]) == NULL and f([ok], sumsq=None) == NULL
         assert f([(P, None, -1, 0)]) == DIMS and f([(P, None, 5, 9)]) == UNSUPPORTED
         assert f([(P + 2, None, 5, 0)]) == ALIGN and f([(P + 1, None, 5, 1)]) == ALIGN and f([ok], sumsq=P + 4) == ALIGN
-        assert f([ok, ok]) == UNSUPPORTED and f([(P + 396, None, 8, 1), ok]) == UNSUPPORTED
+        assert f([(P, None, 2 ** 40, 0), (P + 2 ** 43, None, 1, 0)]) == DIMS
     assert norm([ok], ws=None) == NULL and norm([ok], ws=P + 8) == ALIGN and norm([ok], size=8) == WORKSPACE
+    assert clip([ok, ok]) == UNSUPPORTED and clip([(P + 396, None, 8, 1), ok]) == UNSUPPORTED
     assert clip([ok], max_norm=-1.0) == DIMS and clip([ok], max_norm=float("nan")) == DIMS and clip([ok], out=P + 2) == ALIGN
     assert clip([(P, P + 40, 100, 0)]) == UNSUPPORTED                      # output over its own gradient, shifted
     assert clip([ok, (Q, P, 10, 0)]) == UNSUPPORTED                        # output over another gradient
