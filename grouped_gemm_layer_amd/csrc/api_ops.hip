@@ -167,7 +167,12 @@ moe_status moe_mxfp4_product(const uint8_t* a_codes, const uint8_t* a_scales, in
     return MOE_ERR_ALIGN;
   Mx4Args a{};
   a.a = a_codes; a.sa = a_scales; a.b = b_codes; a.sb = b_scales;
-  a.offsets = offsets; a.row_map = row_map; a.row_div = row_div;
+  a.offsets = offsets; a.row_map = row_map;
+  // 2^(31+s) / row_div rounded up, 2^s >= row_div: the quotients of 31-bit numbers are exact
+  int s = 0;
+  while (((int64_t)1 << s) < row_div) ++s;
+  a.div_shift = 31 + s;
+  a.div_mul = (uint32_t)((((uint64_t)1 << (31 + s)) + (uint64_t)row_div - 1) / (uint64_t)row_div);
   a.c = c; a.ldc = ldc; a.c_bf16 = c_type == MOE_TYPE_BF16;
   a.a_rows = a_rows; a.a_fp8 = a_format == MOE_MX_FP8;
   a.E = E; a.N = N; a.K = K; a.KB = (int)kb; a.rows = rows;

@@ -89,12 +89,15 @@ __device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int lane, Pi
   return true;
 }
 
+// f / row_div by the multiplier and shift the host chose (f < 2^31; exact)
+__device__ __forceinline__ int div_by(uint32_t f, uint32_t mul, int shift) { return (int)(((uint64_t)f * mul) >> shift); }
+
 // A's row of row r of c, or -1 (reads as zeros)
 __device__ __forceinline__ int a_row(const Mx4Args& a, int r) {
   int s = r;
   if (a.row_map) {
     const int f = a.row_map[r];
-    s = f < 0 ? -1 : (int)((uint32_t)f / (uint32_t)a.row_div);
+    s = f < 0 ? -1 : div_by((uint32_t)f, a.div_mul, a.div_shift);
   }
   return (uint32_t)s < (uint32_t)a.a_rows ? s : -1;
 }
@@ -233,22 +236,35 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
 }
 
 // ---------------------------------------------------------------------------
-// Many rows per expert: BM x BN tiles, operands through LDS.
+// Many rows per expert: BM x BN tiles, operands through LDS, resident blocks
+// that walk over the tiles.
 //
 // K advances by stages of KST (256 with MXFP4 rows, 128 with MXFP8: either way
 // 128 bytes, a whole line, per row of A).  Two stages of LDS: while one is
 // multiplied, the other receives the next by buffer-to-LDS DMA (16 bytes a
 // lane; lanes outside a row, its K or the tile read zeros through an
-// out-of-range offset).  One barrier per stage.  Code rows are cut in 16-byte
-// chunks, XOR-swizzled within 128 bytes, so that a fragment's 64 chunks cover
-// every bank equally; with MXFP8 rows, B's 64-byte rows lie in pairs.
+// out-of-range offset).  Code rows are cut in 16-byte chunks, XOR-swizzled
+// within 128 bytes, so that a fragment's 64 chunks cover every bank equally;
+// with MXFP8 rows, B's 64-byte rows lie in pairs.
 //
-// Scales: thread t owns row t of the stage's BM + BN rows, loads its 8 (4)
-// bytes of the next stage into a register and, after the products, writes them
-// to LDS in the order the lanes consume them: lane (r, g) of wave row w finds
-// the bytes of its FM row blocks and both K steps side by side, so one LDS read
-// per operand and stage brings them all, and the instruction's byte select
-// picks each one.
+// A unit is one MFMA step of K (SS of them per stage): FM rows of FN products a
+// wave.  Its fragments are read ahead: A's three rows before their use (ring of
+// four), B's during the unit before (two sets).  Row PB of a stage's last unit,
+// where the wave's last read of the stage has been issued, is the stage's only
+// barrier: it publishes the next stage and frees this one, into which the DMA
+// of the stage after the next then runs, DPR instructions a row.  Reads, DMA
+// and products of all rows so overlap.  The stages of consecutive tiles follow
+// each other without a gap: the next tile's operands arrive while this one's
+// last products run and its results leave (through a piece of LDS of each
+// wave's own, no barrier), which hides the output's HBM time; a block per tile
+// (with 8 waves and two barriers a stage) took 334 us for the 131072 x 1536 x
+// 2048 product of 128 experts, of which its output cost 92.
+//
+// Scales: a thread owns SR of the stage's BM + BN rows, loads their 8 (4) bytes
+// with the DMA into registers and writes them to LDS before the barrier, in the
+// order the lanes consume them: lane (r, g) of wave row w finds the bytes of
+// its FM row blocks and both K steps side by side, so one LDS read per operand
+// and stage brings them all, and the instruction's byte select picks each one.
 // ---------------------------------------------------------------------------
 template <int N, class F, int... I>
 __device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
@@ -259,232 +275,541 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl<N>(f, std::make_integer_sequence<int, N>{});
 }
 
-template <bool FP8_, int BM_, int BN_, int WGM_, int WGN_>
+// The stage's code has no branch that the compiler sees: across blocks it moves products away from their operands'
+// reads and runs out of registers.  What depends on the stage branches inside asm statements.  With one wave on a
+// SIMD every instruction beside the products counts (an MXFP4 product leaves room for three), so they are few: the
+// K offset of a DMA goes through the instruction's scalar offset.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// DMA of W bytes a lane into lds0 + LDS (off outside the buffer: zeros), if go != 0
+template <int W, int LDS>
+__device__ __forceinline__ void dma_if(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t k, uint32_t lds0, int go) {
+  if constexpr (W == 16)
+    asm volatile("s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lnodma%=\n\ts_add_u32 m0, %3, %5\n\t"
+                 "buffer_load_dwordx4 %0, %1, %2 offen lds\n.Lnodma%=:"
+                 :: "v"(off), "s"(r), "s"(k), "s"(lds0), "s"(go), "n"(LDS) : "memory", "m0", "scc");
+  else
+    asm volatile("s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lnodma%=\n\ts_add_u32 m0, %3, %5\n\t"
+                 "buffer_load_dword %0, %1, %2 offen lds\n.Lnodma%=:"
+                 :: "v"(off), "s"(r), "s"(k), "s"(lds0), "s"(go), "n"(LDS) : "memory", "m0", "scc");
+}
+template <int W, int LDS>
+__device__ __forceinline__ void dma_to(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t k, uint32_t lds0) {
+  if constexpr (W == 16)
+    asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(off), "s"(r), "s"(k), "s"(lds0), "n"(LDS) : "memory", "m0", "scc");
+  else
+    asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 :: "v"(off), "s"(r), "s"(k), "s"(lds0), "n"(LDS) : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+// d = s in place if left == 0, four or one at a time
+__device__ __forceinline__ void move4_if(uint32_t* d, const uint32_t* s, int left) {
+  asm("s_cmp_lg_u32 %8, 0\n\ts_cbranch_scc1 .Lnomove%=\n\tv_mov_b32 %0, %4\n\tv_mov_b32 %1, %5\n\tv_mov_b32 %2, %6\n\t"
+      "v_mov_b32 %3, %7\n.Lnomove%=:"
+      : "+v"(d[0]), "+v"(d[1]), "+v"(d[2]), "+v"(d[3]) : "v"(s[0]), "v"(s[1]), "v"(s[2]), "v"(s[3]), "s"(left) : "scc");
+}
+template <int N>
+__device__ __forceinline__ void move_if(uint32_t (&d)[N], const uint32_t (&s)[N], int left) {
+#pragma unroll
+  for (int i = 0; i + 4 <= N; i += 4) move4_if(d + i, s + i, left);
+#pragma unroll
+  for (int i = N / 4 * 4; i < N; ++i) d[i] = left == 0 ? s[i] : d[i];
+}
+// the wait for all vector memory operations, or when kt == 0 for all but the youngest N
+template <int N>
+__device__ __forceinline__ void vm_wait_if(int kt) {
+  asm volatile("s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lsome%=\n\ts_waitcnt vmcnt(0)\n.Lsome%=:\n\ts_waitcnt vmcnt(%1)"
+               :: "s"(kt), "n"(N) : "memory", "scc");
+}
+
+template <bool FP8_, bool SC4_, int BM_, int BN_, int WGM_, int WGN_, int PER_CU_>
 struct Mx4Cfg {
-  static constexpr bool FP8 = FP8_;
+  static constexpr bool FP8 = FP8_, SC4 = SC4_;
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
+  static constexpr int PER_CU = PER_CU_;                 // resident blocks per compute unit
   static constexpr int NW = WGM * WGN, NTHR = 64 * NW;
+  static constexpr int WPE = PER_CU * NW / 4;            // waves per SIMD
   static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
+  static constexpr bool ACC = FM * FN == 64;
   static constexpr int KST = FP8 ? 128 : 256;            // K per stage
-  static constexpr int SS = KST / KSTEP;                 // MFMA steps per stage
+  static constexpr int SS = KST / KSTEP;                 // units per stage
   static constexpr int RA = 128, RB = KST / 2;           // code bytes per row and stage
   static constexpr int SB = KST / 32;                    // scale bytes per row and stage
   static constexpr int A_BYTES = BM * RA, B_BYTES = BN * RB;
-  static constexpr int DA = A_BYTES / 1024 / NW, DB = B_BYTES / 1024 / NW;   // 1 KiB DMAs per wave
+  static constexpr int DA = A_BYTES / 1024 / NW, DB = B_BYTES / 1024 / NW;   // 1 KiB DMAs per wave and stage
   static constexpr int A_SC = A_BYTES + B_BYTES, B_SC = A_SC + BM * SB;
   static constexpr int STAGE = B_SC + BN * SB;
-  static constexpr int LDS = 2 * STAGE;
+  static constexpr int SR = (BM + BN) / NTHR;            // scale rows per thread; groups of 64 of them per wave
+  static constexpr int DS = SC4 ? SR * SS : 0;           // 256-byte DMAs of scales per wave and stage
+  static constexpr int D = DA + DB + DS;
+  static constexpr int PB = FM - 3;                      // row of the barrier
+  static constexpr int DPR = 3;                          // DMAs per row of products
+  static constexpr int D_TAIL = (FM - PB) * DPR;         // DMAs of a stage issued before the next one begins
+  static constexpr int PB_FIRST = SS == 1 ? PB - 1 : FM; // rows of a stage's first unit that may issue the others
+  static constexpr int OUT_ROW = WN * 2, OUT_WAVE = 16 * OUT_ROW;   // bytes of a wave's output in LDS: 16 rows
+  // stores of a whole tile by a wave: 16 bytes a lane, twice as many of fp32 (which bf16's number waits for too)
+  static constexpr int OUT_STORES = WM * WN * 2 / 1024;
+  static constexpr int TILES = 64;                       // tiles listed at a time
+  static constexpr int OUT0 = 2 * STAGE, LIST0 = OUT0 + NW * OUT_WAVE, ROWS0 = LIST0 + TILES * 16;
+  static constexpr int LDS = ROWS0 + 2 * BM * 4;
   static_assert(DA * NW * 1024 == A_BYTES && DB * NW * 1024 == B_BYTES, "whole DMAs per wave");
-  static_assert(BM + BN == NTHR, "one scale row per thread");
-  static_assert(FM * SS % 4 == 0 && FN * SS % 4 == 0, "whole words of scales per lane");
+  static_assert(SR * NTHR == BM + BN && BM == BN && SR <= 2, "scale rows: one of each operand per thread, or of one");
+  static_assert(FM % 4 == 0 && FN == FM && WM == WN, "whole 16-byte pieces of scales per lane");
+  static_assert(PB >= 1, "ring of four A fragments");
+  static_assert(D - D_TAIL <= PB_FIRST * DPR, "the other DMAs fit before the next barrier");
+  static_assert(NW * OUT_WAVE >= 513 * 4, "the prefix sums fit where the output is staged");
+  static_assert(LDS * PER_CU <= 160 * 1024, "LDS of a compute unit");
 };
 
 template <class C>
-__global__ __launch_bounds__(C::NTHR) void mx4_tile_kernel(Mx4Args a, int n_tiles) {
+__global__ __launch_bounds__(C::NTHR) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE)))
+void mx4_tile_kernel(Mx4Args a, int n_tiles) {
   constexpr int BM = C::BM, BN = C::BN, WM = C::WM, WN = C::WN, FM = C::FM, FN = C::FN, NW = C::NW, SS = C::SS;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WGN, wn = wave % C::WGN;
   const int g = lane >> 4, rl = lane & 15;
-  // block b runs on XCD b % 8; each XCD takes a contiguous run of the tiles, column tiles fastest, so that
-  // the tiles sharing an expert's rows and weights meet in one L2
-  int e, m0, mlim, nt;
-  const bool live = find_tile(a, BM, lane, [&](int total) {
+
+  // ---------------- this block's tiles: (expert, first row, row limit, column tile), TILES at a time in LDS.
+  // Block b runs on XCD b % 8; each XCD takes a contiguous run of the tiles (column tiles fastest), its blocks
+  // deal them out in turn, so that those sharing an expert's rows and weights meet in one L2.  The tiles are
+  // counted from the offsets, cut to [0, rows] so that no index leaves c.
+  int4* const s_list = reinterpret_cast<int4*>(smem + C::LIST0);
+  int* const s_pre = reinterpret_cast<int*>(smem + C::OUT0);   // tiles of the experts up to each one
+  auto row_at = [&](int e) { return min(max(a.offsets[e], 0), a.rows); };
+  auto list_tiles = [&](int it0) {
+    int total;
+    __syncthreads();
+    if (a.offsets) {
+      for (int e = tid; e < 512; e += C::NTHR) {
+        int n = 0;
+        if (e < a.E) n = max(0, row_at(e + 1) - row_at(e) + BM - 1) / BM;
+        s_pre[e] = n;
+      }
+      __syncthreads();
+      if (wave == 0) {   // inclusive prefix sums, 8 experts a lane
+        int v[8], sum = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) { sum += s_pre[lane * 8 + q]; v[q] = sum; }
+        int inc = sum;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int u = __shfl_up(inc, off);
+          if (lane >= off) inc += u;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s_pre[lane * 8 + q] = v[q] + inc - sum;
+      }
+      __syncthreads();
+      total = s_pre[a.E - 1];
+    } else {
+      total = (a.rows + BM - 1) / BM;
+    }
     const int64_t tiles = (int64_t)total * n_tiles;
-    const int per_xcd = (int)((tiles + gg::NXCD - 1) / gg::NXCD);
-    const int x = blockIdx.x % gg::NXCD, j = blockIdx.x / gg::NXCD;
-    const int64_t L = (int64_t)x * per_xcd + j;
-    if (j >= per_xcd || L >= tiles) return INT32_MAX;
-    nt = (int)(L % n_tiles);
-    return (int)(L / n_tiles);
-  }, e, m0, mlim);
-  if (!live) return;
-  const int n0 = nt * BN;
+    const int64_t per_xcd = (tiles + gg::NXCD - 1) / gg::NXCD;
+    const int x = blockIdx.x % gg::NXCD, slot = blockIdx.x / gg::NXCD, slots = gridDim.x / gg::NXCD;
+    if (tid < C::TILES) {
+      const int64_t j = slot + (int64_t)(it0 + tid) * slots, L = x * per_xcd + j;
+      int4 t = make_int4(-1, 0, 0, 0);
+      if (j < per_xcd && L < tiles) {
+        const int i = (int)(L / n_tiles);
+        t.w = (int)(L - (int64_t)i * n_tiles);
+        if (a.offsets) {
+          int lo = 0, hi = a.E - 1;             // first expert whose prefix passes i
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pre[mid] > i) hi = mid; else lo = mid + 1;
+          }
+          t.x = lo;
+          t.y = row_at(lo) + (i - (lo > 0 ? s_pre[lo - 1] : 0)) * BM;
+          t.z = row_at(lo + 1);
+        } else {
+          t.x = 0;
+          t.y = i * BM;
+          t.z = a.rows;
+        }
+      }
+      s_list[tid] = t;
+    }
+    __syncthreads();
+  };
+  struct Tile { int e, m0, mlim, n0; };
+  auto tile_at = [&](int it) -> Tile {
+    const int4 t = s_list[it % C::TILES];
+    return Tile{__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y),
+                __builtin_amdgcn_readfirstlane(t.z), __builtin_amdgcn_readfirstlane(t.w) * BN};
+  };
 
+  // ---------------- operands
   const uint32_t pb = (uint32_t)a.KB * 16, pa = C::FP8 ? (uint32_t)a.K : pb;   // code bytes of a row
-  const auto rb = make_rsrc(a.b + (size_t)e * a.N * pb, (uint32_t)a.N * pb);
   const auto ra = make_rsrc(a.a, (uint32_t)a.a_rows * pa);
-  const int nk = (a.K + C::KST - 1) / C::KST;
-
-  // DMA i of wave w fills the 1 KiB block ci = i * NW + w of an operand: lane l
-  // writes 16 bytes at 16 l, which hold chunk `col` of row `row` of that block
-  const int line = lane >> 3, phys = lane & 7, chunk8 = phys ^ line;
+  const int nk = max(2, (a.K + C::KST - 1) / C::KST);   // at least two: the DMA runs two stages ahead, into the next tile at most
+  // DMA i of wave w fills the 1 KiB block ci = i * NW + w of an operand: lane l writes 16 bytes at 16 l
+  const int line = lane >> 3, chunk8 = (lane & 7) ^ line;
   const uint32_t cola = 16u * chunk8;                                          // 8 rows of 128 bytes
   const uint32_t colb = C::RB == 128 ? 16u * chunk8 : 16u * (chunk8 & 3);      // or 16 rows of 64
-  uint32_t oa[C::DA], ob[C::DB];
-#pragma unroll
-  for (int i = 0; i < C::DA; ++i) {
-    const int m = m0 + 8 * (i * NW + wave) + line;
-    const int s = m < mlim ? a_row(a, m) : -1;
-    oa[i] = s >= 0 ? (uint32_t)s * pa + cola : OOB;
-  }
-#pragma unroll
-  for (int i = 0; i < C::DB; ++i) {
-    const int ci = i * NW + wave;
-    const int n = n0 + (C::RB == 128 ? 8 * ci + line : 16 * ci + 2 * line + (chunk8 >> 2));
-    ob[i] = n < a.N ? (uint32_t)n * pb + colb : OOB;
-  }
-  const uint32_t lds0 = (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)smem;
-  auto issue = [&](int kt, int st) __attribute__((always_inline)) {
-    const uint32_t base = lds0 + (uint32_t)(st * C::STAGE);
-    const uint32_t ka = (uint32_t)kt * C::RA, kb = (uint32_t)kt * C::RB;
-    const bool in_a = cola + ka < pa, in_b = colb + kb < pb;
-#pragma unroll
-    for (int i = 0; i < C::DA; ++i)
-      gg::dma16(ra, in_a ? oa[i] + ka : OOB, __builtin_amdgcn_readfirstlane(base + (i * NW + wave) * 1024));
-#pragma unroll
-    for (int i = 0; i < C::DB; ++i)
-      gg::dma16(rb, in_b ? ob[i] + kb : OOB, __builtin_amdgcn_readfirstlane(base + C::A_BYTES + (i * NW + wave) * 1024));
-  };
-
-  // this thread's scale row: source, and where its bytes go (stage-relative)
+  const int lineb = C::RB == 128 ? line : 2 * line + (chunk8 >> 2);            // row of B within the block
+  // scale rows of this thread: rows R < BM are A's, the others B's (the same side for all lanes of a wave)
   using sc_t = std::conditional_t<C::SB == 8, uint64_t, uint32_t>;
   typedef sc_t scu_t __attribute__((aligned(1)));
-  const bool sc_b = tid >= BM;
-  const int R = sc_b ? tid - BM : tid;
-  int64_t sc_row = -1, sc_end;
-  const uint8_t* sc_base;
-  if (sc_b) {
-    if (n0 + R < a.N) sc_row = ((int64_t)e * a.N + n0 + R) * a.KB;
-    sc_base = a.sb;
-    sc_end = (int64_t)a.E * a.N * a.KB;
-  } else {
-    const int s = m0 + R < mlim ? a_row(a, m0 + R) : -1;
-    if (s >= 0) sc_row = (int64_t)s * a.KB;
-    sc_base = a.sa;
-    sc_end = (int64_t)a.a_rows * a.KB;
-  }
-  const int WX = sc_b ? WN : WM, FX = sc_b ? FN : FM;
-  const int sc_dst = (sc_b ? C::B_SC : C::A_SC) + (((R / WX) * 16 + R % 16) * 4) * (FX * SS) + ((R % WX) / 16) * SS;
-  // SB scale bytes of stage kt; those past the row's end zero.  The last bytes of the array are read from SB
-  // before its end and shifted down.
-  auto load_scales = [&](int kt) __attribute__((always_inline)) -> sc_t {
-    sc_t v = 0;
-    const int rem = a.KB - kt * C::SB;
-    if (sc_row >= 0) {
-      const int64_t at = sc_row + (int64_t)kt * C::SB, lim = sc_end - C::SB;
-      const int64_t from = at < lim ? at : lim;
-      v = *reinterpret_cast<const scu_t*>(sc_base + from) >> (8 * (int)(at - from));
-    }
-    if (rem < C::SB) v &= ((sc_t)1 << (8 * rem)) - 1;
-    return v;
+  const bool upper = wave * 64 >= BM;
+  auto sc_is_b = [&](int q) { return C::SR > 1 ? q > 0 : upper; };
+  auto sc_r = [&](int q) { return C::SR > 1 || !upper ? tid : tid - BM; };
+  const auto rsa = make_rsrc(a.sa, (uint32_t)a.a_rows * a.KB);
+
+  // The tile being loaded (the loads run up to two stages ahead of the products, into the next tile): the byte
+  // offsets of its operand rows, OOB for a row outside.  Those of A come from s_rows, which holds two tiles' row
+  // offsets: a tile's row_map entries are fetched three tiles ahead, put there two ahead and turned into offsets
+  // one ahead.  A scale word holds four K blocks of one row; in LDS they lie in the order (wave row, r, i) of row
+  // 16 i + r of the wave's, so that a lane reads those of its FM fragments side by side.
+  struct Source {
+    const uint8_t *b, *sb;            // the expert's weights and scales
+    int64_t sb_room;                  // bytes from there to the scales' end
+    uint32_t oa[C::DA], ob[C::DB], os[C::SR];
   };
-  auto store_scales = [&](sc_t v, int st) __attribute__((always_inline)) {
-    uint8_t* p = smem + st * C::STAGE + sc_dst;
+  uint32_t* const s_rows = reinterpret_cast<uint32_t*>(smem + C::ROWS0);
+  int map_v;                          // row_map entry of this thread's row of a tile
+  auto fetch_row = [&](const Tile& t) __attribute__((always_inline)) {
+    const int m = min(t.m0 + tid, max(t.mlim - 1, 0));
+    map_v = a.row_map ? a.row_map[m] : m;
+  };
+  auto put_row = [&](const Tile& t, int it) __attribute__((always_inline)) {
+    const int s = a.row_map ? div_by((uint32_t)map_v, a.div_mul, a.div_shift) : map_v;
+    const bool ok = t.e >= 0 && t.m0 + tid < t.mlim && map_v >= 0 && s < a.a_rows;
+    if (tid < BM) s_rows[(it & 1) * BM + tid] = ok ? (uint32_t)s * pa : OOB;
+  };
+  const int sc_i = ((64 * wave) & (BM - 1)) + lane, sc_at = sc_i / (16 * FM) * WM + 16 * (sc_i % FM) + sc_i / FM % 16;
+  auto aim = [&](const Tile& t, int it, Source& o) __attribute__((always_inline)) {
+    const uint32_t* rows = s_rows + (it & 1) * BM;
+    const int64_t e = max(t.e, 0);
+    const int n_left = t.e >= 0 ? a.N - t.n0 : 0;        // (no column of a tile behind the last)
+    o.b = a.b + e * a.N * pb;
+    o.sb = a.sb + e * a.N * a.KB;
+    o.sb_room = ((int64_t)a.E - e) * a.N * a.KB;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {   // K block q of the step(s): the lanes with g = q
-      if constexpr (SS == 2)
-        *reinterpret_cast<uint16_t*>(p + q * (FX * SS)) = (uint16_t)(((v >> (8 * q)) & 0xFF) | ((v >> (32 + 8 * q)) & 0xFF) << 8);
-      else
-        p[q * FX] = (uint8_t)(v >> (8 * q));
+    for (int i = 0; i < C::DA; ++i) {
+      const uint32_t r = rows[8 * (i * NW + wave) + line];
+      o.oa[i] = r == OOB ? OOB : r + cola;
+    }
+#pragma unroll
+    for (int i = 0; i < C::DB; ++i) {
+      const int n = (C::RB == 128 ? 8 : 16) * (i * NW + wave) + lineb;
+      o.ob[i] = n < n_left ? (uint32_t)(t.n0 + n) * pb + colb : OOB;
+    }
+#pragma unroll
+    for (int q = 0; q < C::SR; ++q) {                    // this lane's scale row (through a register: this thread's)
+      const int R = C::SC4 ? sc_at : sc_r(q);
+      const uint32_t r = rows[R & (BM - 1)];
+      const uint32_t va = r == OOB ? OOB : r >> (C::FP8 ? 5 : 4), vb = R < n_left ? (uint32_t)(t.n0 + R) * a.KB : OOB;
+      o.os[q] = sc_is_b(q) ? vb : va;
+    }
+  };
+  Source src, src_n;
+  auto take_source = [&](int left) __attribute__((always_inline)) {   // the next tile's if no stage of this one is left
+    src.b = left == 0 ? src_n.b : src.b;
+    src.sb = left == 0 ? src_n.sb : src.sb;
+    src.sb_room = left == 0 ? src_n.sb_room : src.sb_room;
+    move_if(src.oa, src_n.oa, left);
+    move_if(src.ob, src_n.ob, left);
+    move_if(src.os, src_n.os, left);
+  };
+  const uint32_t lds0 = (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)smem;
+  const uint32_t lds16 = __builtin_amdgcn_readfirstlane(lds0 + wave * 1024);   // where this wave's DMAs start
+  const uint32_t lds4 = __builtin_amdgcn_readfirstlane(lds0 + (C::SR == 1 && upper ? C::B_SC - C::A_SC : 0) + (64 * wave & (BM - 1)) * 4);
+  // DMA instruction i < D of stage kt: A's codes, B's codes, scales; go == 0 (known only then): not now
+  int dma_kt = 0;                     // stage that the DMA now fills
+  bool in_a = false, in_b = false;    // whether the lane's codes are inside K there
+  auto set_dma = [&](int kt) __attribute__((always_inline)) {
+    dma_kt = kt;
+    in_a = cola + (uint32_t)kt * C::RA < pa;
+    in_b = colb + (uint32_t)kt * C::RB < pb;
+  };
+  auto dma = [&](auto i_, auto sure_, int st, int go) __attribute__((always_inline)) {
+    constexpr int i = i_;
+    const uint32_t half = st ? C::STAGE : 0;
+    auto to = [&](auto w_, auto at_, __amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t k, uint32_t l) __attribute__((always_inline)) {
+      if constexpr (sure_) dma_to<w_, at_>(r, off, k, l); else dma_if<w_, at_>(r, off, k, l, go);
+    };
+    if constexpr (i < C::DA) {
+      to(std::integral_constant<int, 16>{}, std::integral_constant<int, i * NW * 1024>{}, ra, in_a ? src.oa[i] : OOB,
+         (uint32_t)dma_kt * C::RA, lds16 + half);
+    } else if constexpr (i < C::DA + C::DB) {
+      constexpr int q = i - C::DA;
+      to(std::integral_constant<int, 16>{}, std::integral_constant<int, C::A_BYTES + q * NW * 1024>{},
+         make_rsrc(src.b, (uint32_t)a.N * pb), in_b ? src.ob[q] : OOB, (uint32_t)dma_kt * C::RB, lds16 + half);
+    } else {
+      constexpr int q = (i - C::DA - C::DB) / SS, s = (i - C::DA - C::DB) % SS;           // row group, MFMA step
+      const bool b = sc_is_b(q);
+      const uint32_t k = (uint32_t)dma_kt * C::SB + 4 * s;
+      to(std::integral_constant<int, 4>{}, std::integral_constant<int, (q > 0 ? C::B_SC : C::A_SC) + s * BM * 4>{},
+         b ? make_rsrc(src.sb, (uint32_t)a.N * a.KB) : rsa, k < (uint32_t)a.KB ? src.os[q] : OOB, k, lds4 + half);
+    }
+  };
+  // K not a multiple of 128: the words of a row are not aligned, and its scales pass through a register.  SB bytes
+  // of a row for stage kt; those past the row's end, and of a row outside, zero.  The last bytes of the array are
+  // read from SB before its end and shifted down.
+  sc_t sc[C::SR], sc_mask;
+  int sc_fix[C::SR];
+  auto load_scales = [&](int kt) __attribute__((always_inline)) {
+    const int rem = min(max(a.KB - kt * C::SB, 0), C::SB);
+    sc_mask = rem == C::SB ? ~(sc_t)0 : ((sc_t)1 << (8 * rem)) - 1;
+#pragma unroll
+    for (int q = 0; q < C::SR; ++q) {
+      const uint32_t row = src.os[q];
+      const uint8_t* base = sc_is_b(q) ? src.sb : a.sa;
+      const int64_t lim = (sc_is_b(q) ? src.sb_room : (int64_t)a.a_rows * a.KB) - C::SB;
+      // (an expert within SB bytes of the array's end reads from before its own scales: lim < 0)
+      const int64_t at = (row == OOB ? 0 : (int64_t)row) + (int64_t)kt * C::SB, from = min(at, lim);
+      sc[q] = *reinterpret_cast<const scu_t*>(base + from);
+      sc_fix[q] = row == OOB ? 64 : (int)min(at - from, (int64_t)8) * 8;
+    }
+  };
+  auto store_scales = [&](int st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < C::SR; ++q) {
+      const bool b = sc_is_b(q);
+      const sc_t v = sc_fix[q] >= 8 * C::SB ? (sc_t)0 : (sc[q] >> sc_fix[q]) & sc_mask;
+      const int R = sc_r(q), at = (R / WM * 16 + R % 16) * FM + R % WM / 16;
+      uint32_t* p = reinterpret_cast<uint32_t*>(smem + st * C::STAGE + (b ? C::B_SC : C::A_SC)) + at;
+#pragma unroll
+      for (int s = 0; s < SS; ++s) p[s * BM] = (uint32_t)(v >> (32 * (s % SS)));
     }
   };
 
+  // ---------------- fragments
   f32x4_t acc[FM][FN];
+  u32x4_t ar[4], ar_h[C::FP8 ? 4 : 1], br[2][FN];     // (kept as the four words that MXFP4 codes take)
+  uint32_t xa[2][FM], xb[2][FN];                      // scale words, as many sets; byte g counts
+  const int sw = rl & 7;                              // rows of a fragment differ from rl by multiples of 16
+  auto read_a = [&](int st, int s, int i, int slot) __attribute__((always_inline)) {
+    const uint8_t* p = smem + st * C::STAGE + (wm * WM + 16 * i + rl) * 128;
+    ar[slot] = *reinterpret_cast<const u32x4_t*>(p + (((C::FP8 ? g : 4 * s + g) ^ sw) << 4));
+    if constexpr (C::FP8) ar_h[slot] = *reinterpret_cast<const u32x4_t*>(p + (((4 + g) ^ sw) << 4));
+  };
+  auto read_b = [&](int st, int s, int j, int set) __attribute__((always_inline)) {
+    const int row = wn * WN + 16 * j + rl;
+    const uint8_t* p = smem + st * C::STAGE + C::A_BYTES;
+    if constexpr (C::RB == 128) br[set][j] = *reinterpret_cast<const u32x4_t*>(p + row * 128 + (((4 * s + g) ^ sw) << 4));
+    else br[set][j] = *reinterpret_cast<const u32x4_t*>(p + (row >> 1) * 128 + ((((rl & 1) * 4 + g) ^ ((rl >> 1) & 7)) << 4));
+  };
+  auto read_scales = [&](int st, int s, int set) __attribute__((always_inline)) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(smem + st * C::STAGE + C::A_SC) + s * BM + (wm * 16 + rl) * FM;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(smem + st * C::STAGE + C::B_SC) + s * BN + (wn * 16 + rl) * FN;
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i) xa[set][i] = p[i];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const bool idle = m0 + wm * WM >= mlim;   // no row of this wave: it only moves data
+    for (int j = 0; j < FN; ++j) xb[set][j] = q[j];
+  };
 
-  auto multiply = [&](int st) __attribute__((always_inline)) {
-    const uint8_t* base = smem + st * C::STAGE;
-    constexpr int WA = FM * SS / 4, WB = FN * SS / 4;   // words of scales
-    uint32_t xa[WA], xb[WB];
-    const uint32_t* pxa = reinterpret_cast<const uint32_t*>(base + C::A_SC + ((wm * 16 + rl) * 4 + g) * (FM * SS));
-    const uint32_t* pxb = reinterpret_cast<const uint32_t*>(base + C::B_SC + ((wn * 16 + rl) * 4 + g) * (FN * SS));
-#pragma unroll
-    for (int w = 0; w < WA; ++w) xa[w] = pxa[w];
-#pragma unroll
-    for (int w = 0; w < WB; ++w) xb[w] = pxb[w];
-    static_for<SS>([&](auto s_) {
-      constexpr int s = s_;
-      i32x8_t fa[FM], fb[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int row = wn * WN + 16 * j + rl;
-        int off;
-        if constexpr (C::RB == 128) off = row * 128 + (((4 * s + g) ^ (row & 7)) << 4);
-        else off = (row >> 1) * 128 + ((((row & 1) * 4 + g) ^ ((row >> 1) & 7)) << 4);
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(base + C::A_BYTES + off);
-        fb[j] = i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+  // ---------------- state of the walk
+  int it = 0;                       // tile of the products, its stage, and the LDS half that holds it
+  int kt = 0, st = 0;
+  list_tiles(0);
+  Tile cur = tile_at(0), nxt = tile_at(1), nxt2 = tile_at(2);
+  if (cur.e < 0) return;
+
+  // One unit of products: MFMA step s of the stage in half st.
+  auto unit = [&](auto s_) __attribute__((always_inline)) {
+    constexpr int s = s_;
+    constexpr bool LAST = s == SS - 1;              // of the stage
+    constexpr int set = SS == 2 ? s : 0, nset = 1 - set;
+    static_for<FM>([&](auto i_) {
+      constexpr int i = i_;
+      if constexpr (LAST && i == C::PB) {
+        vm_wait_if<C::OUT_STORES>(kt);              // the next stage's DMA has arrived (in a tile's first stage the last
+                                                    // tile's stores, which are younger, may still be under way)
+        if constexpr (!C::SC4) store_scales(st ^ 1);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // this half is free: the stage after the next goes there, the next tile's at the end of this one (zeros
+        // behind the last)
+        take_source(nk - (kt + 2));
+        set_dma(kt + 2 < nk ? kt + 2 : kt + 2 - nk);
+        if constexpr (!C::SC4) load_scales(dma_kt);
+        read_scales(st ^ 1, 0, nset);
       }
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int row = wm * WM + 16 * i + rl;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(base + row * 128 + (((C::FP8 ? g : 4 * s + g) ^ (row & 7)) << 4));
-        u32x4_t h = {0u, 0u, 0u, 0u};
-        if constexpr (C::FP8) h = *reinterpret_cast<const u32x4_t*>(base + row * 128 + (((4 + g) ^ (row & 7)) << 4));
-        fa[i] = i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
-      }
-      static_for<FM>([&](auto i_) {
-        static_for<FN>([&](auto j_) {
-          constexpr int i = i_, j = j_, ia = i * SS + s, ib = j * SS + s;
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              fb[j], fa[i], acc[i][j], FMT_FP4, C::FP8 ? FMT_FP8 : FMT_FP4, ib % 4, (int)xb[ib / 4], ia % 4,
-              (int)xa[ia / 4]);
+      if constexpr (!LAST && i == 0) read_scales(st, s + 1, nset);
+      if constexpr (i + 3 < FM) read_a(st, s, i + 3, (i + 3) % 4);
+      else if constexpr (!LAST) read_a(st, s + 1, i + 3 - FM, (i + 3) % 4);
+      else read_a(st ^ 1, 0, i + 3 - FM, (i + 3) % 4);
+      if constexpr (!LAST) {
+        constexpr int per = (FN + FM - 1) / FM;
+        static_for<per>([&](auto q_) { if constexpr (i * per + q_ < FN) read_b(st, s + 1, i * per + q_, nset); });
+      } else if constexpr (i >= C::PB) {
+        constexpr int per = (FN + FM - C::PB - 1) / (FM - C::PB);
+        static_for<per>([&](auto q_) {
+          if constexpr ((i - C::PB) * per + q_ < FN) read_b(st ^ 1, 0, (i - C::PB) * per + q_, nset);
         });
+      }
+      // the stage's DMAs, DPR a row from the barrier on; the last ones in the next stage's first unit, unless they were
+      // sent before the output
+      constexpr bool head = LAST && i >= C::PB;
+      constexpr int at = head ? i - C::PB : s == 0 && i < C::PB_FIRST ? C::D_TAIL / C::DPR + i : -1;
+      if constexpr (at >= 0) static_for<C::DPR>([&](auto q_) {
+        constexpr int d = at * C::DPR + q_;
+        if constexpr (d < C::D) dma(std::integral_constant<int, d>{}, std::bool_constant<head>{}, head ? st : st ^ 1, kt);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<FN>([&](auto j_) {
+        constexpr int j = j_;
+        const u32x4_t b = br[set][j], x = ar[i % 4], h = C::FP8 ? ar_h[C::FP8 ? i % 4 : 0] : u32x4_t{0u, 0u, 0u, 0u};
+        const i32x8_t fb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+        const i32x8_t fa = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
+        if constexpr (i == 0) xb[set][j] >>= 8 * g;
+        if constexpr (j == 0) xa[set][i] >>= 8 * g;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc[i][j], FMT_FP4,
+                                                                     C::FP8 ? FMT_FP8 : FMT_FP4, 0, (int)xb[set][j], 0,
+                                                                     (int)xa[set][i]);
       });
     });
   };
-
-  sc_t sc = load_scales(0);
-  issue(0, 0);
-  gg::vm_wait<0>();
-  store_scales(sc, 0);
-  __syncthreads();
-  for (int kt = 0; kt < nk; ++kt) {
-    const int st = kt & 1;
-    if (kt + 1 < nk) {
-      sc = load_scales(kt + 1);
-      issue(kt + 1, st ^ 1);
+  auto stage = [&]() __attribute__((always_inline)) {
+    unit(std::integral_constant<int, 0>{});
+    if constexpr (SS == 2) {
+      unit(std::integral_constant<int, 1>{});
+    } else {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) br[0][j] = br[1][j];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) { xb[0][j] = xb[1][j]; xa[0][j] = xa[1][j]; }
     }
-    if (!idle) multiply(st);
-    gg::vm_wait<0>();
-    if (kt + 1 < nk) store_scales(sc, st ^ 1);
-    __syncthreads();
-  }
+    st ^= 1;
+  };
 
-  // the tile leaves through LDS, CH rows at a time, so that the stores run along its rows
-  auto copy_out = [&](auto zero) __attribute__((always_inline)) {
+  // ---------------- results: 16 rows at a time through the wave's own LDS, so that the stores run along the rows.
+  // A whole tile's rows go one step ahead: the next ones' writes and reads of LDS are under way while a row block's
+  // pieces are stored.
+  auto copy_out = [&](auto zero, auto whole_) __attribute__((always_inline)) {
     using T = decltype(zero);
+    constexpr bool WHOLE = whole_;
     constexpr int VT = 16 / (int)sizeof(T);                 // values per 16-byte piece
-    constexpr int NQ = BN / VT, ROWB = BN * (int)sizeof(T);
-    constexpr int CH = BM * ROWB <= C::LDS ? BM : BM * ROWB <= 2 * C::LDS ? BM / 2 : BM / 4;
-    static_assert(CH * ROWB <= C::LDS && CH % 16 == 0, "row chunk fits");
+    constexpr int COLS = C::OUT_ROW / (int)sizeof(T);       // columns that fit at once
+    constexpr int NQ = C::OUT_ROW / 16, RPP = 64 / NQ;      // pieces per row, rows per pass of the wave
+    constexpr int NH = WN / COLS, NC = FM * NH, NP = 16 / RPP;
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));   // keeps what follows from it out of the walk, where it would hold registers
+    const int g = lane >> 4, rl = lane & 15, prow = lane / NQ, piece = lane % NQ;
+    uint8_t* const stg = smem + C::OUT0 + wave * C::OUT_WAVE;
+    const int mw = cur.m0 + wm * WM, nw = cur.n0 + wn * WN;
+    T* const o0 = static_cast<T*>(a.c) + (int64_t)(mw + prow) * a.ldc + nw + piece * VT;
+    auto put = [&](auto c_) __attribute__((always_inline)) {
+      constexpr int i = c_ / NH, h = c_ % NH;
 #pragma unroll
-    for (int ch = 0; ch < BM / CH; ++ch) {
-      if (ch > 0) __syncthreads();
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if ((wm * WM + 16 * i) / CH != ch) continue;        // a 16-row block lies in one chunk
-        const int row = (wm * WM + 16 * i) % CH + rl;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int byte = (wn * WN + 16 * j + 4 * g) * (int)sizeof(T);
-          uint8_t* p = smem + row * ROWB + (((byte >> 4) ^ (row % NQ)) << 4) + (byte & 15);
-          const f32x4_t v = acc[i][j];
-          if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint2*>(p) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
-          else
-            *reinterpret_cast<f32x4_t*>(p) = v;
-        }
+      for (int jj = 0; jj < COLS / 16; ++jj) {
+        if constexpr (C::ACC) asm volatile("" : "+a"(acc[i][h * (COLS / 16) + jj]));   // (not moved before their turn)
+        const f32x4_t v = acc[i][h * (COLS / 16) + jj];
+        const int byte = (16 * jj + 4 * g) * (int)sizeof(T);
+        uint8_t* p = stg + rl * C::OUT_ROW + (((byte >> 4) ^ (rl % NQ)) << 4) + (byte & 15);
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(p) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+        else
+          *reinterpret_cast<f32x4_t*>(p) = v;
       }
-      __syncthreads();
-      T* c = static_cast<T*>(a.c);
-      for (int q0 = tid; q0 < CH * NQ; q0 += C::NTHR) {
-        const int row = q0 / NQ, q = q0 % NQ;
-        const int m = m0 + ch * CH + row, n = n0 + q * VT;
-        const int cnt = min(VT, a.N - n);
-        if (m < mlim && cnt > 0) {
-          const RowVec<T> v = {*reinterpret_cast<const u32x4v_t*>(smem + row * ROWB + ((q ^ (row % NQ)) << 4))};
-          v.store(c + (int64_t)m * a.ldc + n, cnt);
+    };
+    auto at = [&](int q) { return stg + (q * RPP + prow) * C::OUT_ROW + ((piece ^ ((q * RPP + prow) % NQ)) << 4); };
+    if constexpr (WHOLE) {
+      u32x4v_t v[2][NP];
+      auto get = [&](auto c_) __attribute__((always_inline)) {
+        put(c_);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) v[c_ % 2][q] = *reinterpret_cast<const u32x4v_t*>(at(q));
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      get(std::integral_constant<int, 0>{});
+      static_for<NC>([&](auto c_) {
+        constexpr int c = c_;
+        if constexpr (c + 1 < NC) get(std::integral_constant<int, c + 1>{});
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+          *reinterpret_cast<u32x4u_t*>(o0 + (int64_t)(16 * (c / NH) + q * RPP) * a.ldc + c % NH * COLS) = v[c % 2][q];
+      });
+    } else {
+      static_for<NC>([&](auto c_) {
+        constexpr int c = c_;
+        put(c_);
+#pragma nounroll
+        for (int q = 0; q < NP; ++q) {
+          const T* p = reinterpret_cast<const T*>(at(q));
+          T* o = o0 + (int64_t)(16 * (c / NH) + q * RPP) * a.ldc + c % NH * COLS;
+          const int cnt = mw + 16 * (c / NH) + q * RPP + prow < cur.mlim ? a.N - nw - piece * VT - c % NH * COLS : 0;
+          if (cnt >= VT) {
+            *reinterpret_cast<u32x4u_t*>(o) = *reinterpret_cast<const u32x4v_t*>(p);
+          } else if (cnt > 0) {
+#pragma nounroll
+            for (int k = 0; k < cnt; ++k) o[k] = p[k];
+          }
         }
-      }
+      });
     }
   };
-  if (a.c_bf16) copy_out(bf16_t{});
-  else copy_out(float{});
+
+  // ---------------- the walk
+  auto send = [&](auto from_, int st) __attribute__((always_inline)) {   // the stage's DMAs from that one on
+    static_for<C::D>([&](auto i_) {
+      if constexpr (i_ >= from_) dma(i_, std::true_type{}, st, 1);
+    });
+  };
+  constexpr std::integral_constant<int, 0> all{};
+  constexpr std::integral_constant<int, C::D_TAIL> rest{};
+  fetch_row(cur);
+  put_row(cur, 0);
+  fetch_row(nxt);
+  put_row(nxt, 1);
+  fetch_row(nxt2);
+  __syncthreads();
+  aim(cur, 0, src);
+  if constexpr (!C::SC4) {
+    load_scales(0);
+    store_scales(0);
+    load_scales(1);
+  }
+  set_dma(0);
+  send(all, 0);
+  set_dma(1);
+  send(all, 1);
+  gg::vm_wait<0>();
+  __syncthreads();
+  read_scales(0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) read_b(0, 0, j, 0);
+  read_a(0, 0, 0, 0);
+  read_a(0, 0, 1, 1);
+  read_a(0, 0, 2, 2);
+  for (;;) {
+    if ((it + 3) % C::TILES == 0) list_tiles(it + 3);   // (the waves' staged output has been read by then)
+    aim(nxt, it + 1, src_n);
+    put_row(nxt2, it + 2);
+    const Tile nxt3 = tile_at(it + 3);
+    fetch_row(nxt3);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        // 64 fragments fill the accumulation registers to the last one: named here as their place, or the
+        // compiler deals them over both kinds of registers and moves hundreds in every stage
+        if constexpr (C::ACC) asm volatile("" : "+a"(acc[i][j]));
+      }
+#pragma nounroll
+    for (kt = 0; kt < nk; ++kt) stage();
+    send(rest, st ^ 1);           // the rest of the next tile's second stage, ahead of the stores
+    if (cur.m0 + (wm + 1) * WM <= cur.mlim && cur.n0 + (wn + 1) * WN <= a.N) {
+      if (a.c_bf16) copy_out(bf16_t{}, std::true_type{});
+      else copy_out(float{}, std::true_type{});
+    } else {
+      if (a.c_bf16) copy_out(bf16_t{}, std::false_type{});
+      else copy_out(float{}, std::false_type{});
+      gg::vm_wait<0>();           // (fewer stores than the next tile's first wait allows for)
+    }
+    if (nxt.e < 0) break;
+    cur = nxt;
+    nxt = nxt2;
+    nxt2 = nxt3;
+    ++it;
+  }
+  gg::vm_wait<0>();   // no DMA is under way when the block gives its LDS back
 }
 
 // row tiles of height bm at most: every expert with rows ends in a partial one
@@ -506,17 +831,18 @@ template <class C>
 hipError_t launch_tiles(const Mx4Args& a, hipStream_t s) {
   const int n_tiles = (a.N + C::BN - 1) / C::BN;
   const int64_t tiles = max_tiles(a, C::BM) * n_tiles;
-  const int64_t grid = (tiles + gg::NXCD - 1) / gg::NXCD * gg::NXCD;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return launch_kernel(mx4_tile_kernel<C>, dim3((unsigned)grid), dim3(C::NTHR), 0, s, a, n_tiles);
+  const int64_t all = (tiles + gg::NXCD - 1) / gg::NXCD * gg::NXCD, resident = resident_blocks(C::PER_CU);
+  return launch_kernel(mx4_tile_kernel<C>, dim3((unsigned)(all < resident ? all : resident)), dim3(C::NTHR), 0, s, a,
+                       n_tiles);
 }
 
 template <bool FP8, bool SC4>
 hipError_t launch_formats(const Mx4Args& a, hipStream_t s) {
-  // the tile kernel reads scales 8 bytes at a time and needs that many in each array
-  const bool room = (int64_t)a.a_rows * a.KB >= 8 && (int64_t)a.E * a.N * a.KB >= 8;
-  if (room && a.rows / a.E >= MX4_BIG) return launch_tiles<Mx4Cfg<FP8, 256, 256, 2, 4>>(a, s);
-  if (room && a.rows / a.E >= MX4_MID) return launch_tiles<Mx4Cfg<FP8, 128, 128, 2, 2>>(a, s);
+  // scales that pass through registers are read 8 bytes at a time: that many in each array
+  const bool room = SC4 || ((int64_t)a.a_rows * a.KB >= 8 && (int64_t)a.E * a.N * a.KB >= 8);
+  if constexpr (SC4)
+    if (a.rows / a.E >= MX4_BIG) return launch_tiles<Mx4Cfg<FP8, SC4, 256, 256, 2, 2, 1>>(a, s);
+  if (room && a.rows / a.E >= MX4_MID) return launch_tiles<Mx4Cfg<FP8, SC4, 128, 128, 2, 2, 2>>(a, s);
   return launch_stream<FP8, SC4, 1, 4>(a, s);
 }
 

@@ -286,7 +286,9 @@ struct Mx4Args {
   const int32_t* row_map;         // [rows] or null
   void* c;
   int64_t ldc;
-  int a_rows, a_fp8, E, N, K, KB, row_div, rows, c_bf16;
+  int a_rows, a_fp8, E, N, K, KB, rows, c_bf16;
+  uint32_t div_mul;               // row_map[r] / row_div = (row_map[r] * div_mul) >> div_shift
+  int div_shift;
 };
 hipError_t launch_mx4_product(const Mx4Args& a, hipStream_t s);
 // gradient norm and clipping (gradnorm.hip)
