@@ -20,13 +20,6 @@ using gg::make_rsrc;
 using gg::u32x4_t;
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 
-#ifndef MOE_MX4_BIG
-#define MOE_MX4_BIG 256
-#endif
-#ifndef MOE_MX4_MID
-#define MOE_MX4_MID 32
-#endif
-constexpr int MX4_BIG = MOE_MX4_BIG, MX4_MID = MOE_MX4_MID;
 constexpr int KSTEP = 128;   // K of one scaled MFMA
 constexpr int FMT_FP8 = 0, FMT_FP4 = 4;   // format fields of the instruction
 
@@ -35,14 +28,10 @@ constexpr int FMT_FP8 = 0, FMT_FP4 = 4;   // format fields of the instruction
 // experts l*per .. of the offsets, a prefix sum over the lanes and a ballot
 // give the lane that holds tile i.  That takes about 0.5 us of a tile's time
 // and saves the launch that would build a table.  Offsets are cut to [0, rows]
-// so that no index leaves c.  `pick` gives i from the number of tiles; false
-// when that is no tile.
-template <class Pick>
-__device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int lane, Pick&& pick, int& e, int& m0,
-                                          int& mlim) {
+// so that no index leaves c.  False when i is no tile.
+__device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int lane, int i, int& e, int& m0, int& mlim) {
   if (a.offsets == nullptr) {
-    const int total = (a.rows + bm - 1) / bm, i = pick(total);
-    if (i >= total) return false;
+    if (i >= (a.rows + bm - 1) / bm) return false;
     e = 0;
     m0 = i * bm;
     mlim = a.rows;
@@ -68,7 +57,6 @@ __device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int lane, Pi
     const int v = __shfl_up(inc, off);
     if (lane >= off) inc += v;
   }
-  const int i = pick(__builtin_amdgcn_readlane(inc, 63));
   const uint64_t hit = __ballot(inc > i);
   if (hit == 0) return false;
   const int src = __builtin_ctzll(hit);
@@ -126,55 +114,44 @@ __device__ __forceinline__ void store4(const Mx4Args& a, int m, int n, f32x4_t v
 }
 
 // ---------------------------------------------------------------------------
-// Few rows per expert: the weights are read once, straight into registers
-// (each byte has one reader, so LDS would only add a stop), by as many waves as
-// possible: a wave takes MF x 16 rows and 16 columns.  KS waves of a block
-// split K and add their sums in wave order through LDS, for few columns.
+// Few rows per expert: the weights go straight into registers (each byte has
+// one reader, so LDS would only add a stop).  A block takes 16 rows and 16
+// columns; its four waves split K, so that even one expert's weights are read
+// by many waves, and their sums are added in wave order through LDS.
 // SC4: KB % 4 == 0, a K step's four scale bytes of a row are one aligned word.
 // ---------------------------------------------------------------------------
-template <bool FP8, bool SC4, int MF, int KS>
+template <bool FP8, bool SC4>
 __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups) {
+  constexpr int NW = 4;
   constexpr int U = 4;                         // K steps whose loads are in flight together
-  constexpr int NWV = 4 / KS;                  // waves along the columns
-  __shared__ f32x4_t s_acc[KS > 1 ? KS - 1 : 1][KS > 1 ? MF : 1][64];
+  __shared__ f32x4_t s_acc[NW - 1][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, rl = lane & 15;
-  const int tile = blockIdx.x / n_groups, ng = blockIdx.x % n_groups;
+  const int tile = blockIdx.x / n_groups, n0 = blockIdx.x % n_groups * 16;
   int e, m0, mlim;
-  if (!find_tile(a, 16 * MF, lane, [&](int) { return tile; }, e, m0, mlim)) return;
-  const int wk = KS > 1 ? wave : 0, wn = KS > 1 ? 0 : wave;
-  const int n0 = (ng * NWV + wn) * 16;
+  if (!find_tile(a, 16, lane, tile, e, m0, mlim)) return;
   const uint32_t pb = (uint32_t)a.KB * 16, pa = FP8 ? (uint32_t)a.K : pb;   // code bytes of a row
   const auto rb = make_rsrc(a.b + (size_t)e * a.N * pb, (uint32_t)a.N * pb);
   const auto rsb = make_rsrc(a.sb + (size_t)e * a.N * a.KB, (uint32_t)a.N * a.KB);
   const auto ra = make_rsrc(a.a, (uint32_t)a.a_rows * pa);
   const auto rsa = make_rsrc(a.sa, (uint32_t)a.a_rows * a.KB);
-  const int nb = n0 + rl;
+  const int nb = n0 + rl, m = m0 + rl;
   const bool nok = nb < a.N;
   const uint32_t ob = nok ? (uint32_t)nb * pb : 0, osb = nok ? (uint32_t)nb * a.KB : 0;
-  uint32_t oa[MF], osa[MF];
-  bool mok[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int m = m0 + 16 * i + rl;
-    const int s = m < mlim ? a_row(a, m) : -1;
-    mok[i] = s >= 0;
-    oa[i] = mok[i] ? (uint32_t)s * pa : 0;
-    osa[i] = mok[i] ? (uint32_t)s * a.KB : 0;
-  }
-  f32x4_t acc[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int row = m < mlim ? a_row(a, m) : -1;
+  const bool mok = row >= 0;
+  const uint32_t oa = mok ? (uint32_t)row * pa : 0, osa = mok ? (uint32_t)row * a.KB : 0;
+  f32x4_t acc{0.f, 0.f, 0.f, 0.f};
   const int nk = (a.K + KSTEP - 1) / KSTEP;
-  const int per = (nk + KS - 1) / KS;
-  const int k0 = wk * per, k1 = min(nk, k0 + per);
+  const int per = (nk + NW - 1) / NW;
+  const int k0 = wave * per, k1 = min(nk, k0 + per);
   auto scale = [&](__amdgpu_buffer_rsrc_t r, uint32_t row, bool ok, int kt) -> int {
     if constexpr (SC4) return __builtin_amdgcn_raw_buffer_load_b32(r, ok ? row + 4 * kt : OOB, 0, 0);
     else return __builtin_amdgcn_raw_buffer_load_b8(r, ok && 4 * kt + g < a.KB ? row + 4 * kt + g : OOB, 0, 0);
   };
   for (int kt0 = k0; kt0 < k1; kt0 += U) {
-    u32x4_t cb[U], ca[U][MF], cah[U][FP8 ? MF : 1];
-    int sb[U], sa[U][MF];
+    u32x4_t cb[U], ca[U], cah[U];
+    int sb[U], sa[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kt = kt0 + u;
@@ -187,52 +164,30 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
     for (int u = 0; u < U; ++u) {
       const int kt = kt0 + u;
       const bool in = kt < k1;
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        if constexpr (FP8) {
-          const uint32_t ka = (uint32_t)kt * 128 + 16 * g;
-          ca[u][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, in && mok[i] && ka < pa ? oa[i] + ka : OOB, 0, 0);
-          cah[u][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, in && mok[i] && ka + 64 < pa ? oa[i] + ka + 64 : OOB, 0, 0);
-        } else {
-          const uint32_t ka = (uint32_t)kt * 64 + 16 * g;
-          ca[u][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, in && mok[i] && ka < pa ? oa[i] + ka : OOB, 0, 0);
-        }
-        sa[u][i] = scale(rsa, osa[i], in && mok[i], kt);
-      }
+      const uint32_t ka = (uint32_t)kt * (FP8 ? 128 : 64) + 16 * g;
+      ca[u] = __builtin_amdgcn_raw_buffer_load_b128(ra, in && mok && ka < pa ? oa + ka : OOB, 0, 0);
+      if constexpr (FP8)
+        cah[u] = __builtin_amdgcn_raw_buffer_load_b128(ra, in && mok && ka + 64 < pa ? oa + ka + 64 : OOB, 0, 0);
+      else
+        cah[u] = u32x4_t{0u, 0u, 0u, 0u};
+      sa[u] = scale(rsa, osa, in && mok, kt);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const i32x8_t fb = {(int)cb[u][0], (int)cb[u][1], (int)cb[u][2], (int)cb[u][3], 0, 0, 0, 0};
-      const int xb = SC4 ? (int)((uint32_t)sb[u] >> (8 * g)) : sb[u];
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        i32x8_t fa = {(int)ca[u][i][0], (int)ca[u][i][1], (int)ca[u][i][2], (int)ca[u][i][3], 0, 0, 0, 0};
-        if constexpr (FP8) {
-          fa[4] = (int)cah[u][i][0]; fa[5] = (int)cah[u][i][1]; fa[6] = (int)cah[u][i][2]; fa[7] = (int)cah[u][i][3];
-        }
-        const int xa = SC4 ? (int)((uint32_t)sa[u][i] >> (8 * g)) : sa[u][i];
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc[i], FMT_FP4, FP8 ? FMT_FP8 : FMT_FP4, 0,
-                                                                  xb, 0, xa);
-      }
+      const i32x8_t fa = {(int)ca[u][0], (int)ca[u][1], (int)ca[u][2], (int)ca[u][3],
+                          (int)cah[u][0], (int)cah[u][1], (int)cah[u][2], (int)cah[u][3]};
+      const int xb = SC4 ? (int)((uint32_t)sb[u] >> (8 * g)) : sb[u], xa = SC4 ? (int)((uint32_t)sa[u] >> (8 * g)) : sa[u];
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc, FMT_FP4, FP8 ? FMT_FP8 : FMT_FP4, 0, xb, 0, xa);
     }
   }
-  if constexpr (KS > 1) {
-    if (wave > 0) {
+  if (wave > 0) s_acc[wave - 1][lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
 #pragma unroll
-      for (int i = 0; i < MF; ++i) s_acc[wave - 1][i][lane] = acc[i];
-    }
-    __syncthreads();
-    if (wave > 0) return;
-#pragma unroll
-    for (int w = 0; w < KS - 1; ++w)
-#pragma unroll
-      for (int i = 0; i < MF; ++i) acc[i] += s_acc[w][i][lane];
-  }
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int m = m0 + 16 * i + rl, n = n0 + 4 * g;
-    if (m < mlim && n < a.N) store4(a, m, n, acc[i]);
-  }
+  for (int w = 0; w < NW - 1; ++w) acc += s_acc[w][lane];
+  const int n = n0 + 4 * g;
+  if (m < mlim && n < a.N) store4(a, m, n, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -255,16 +210,22 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
 // of the stage after the next then runs, DPR instructions a row.  Reads, DMA
 // and products of all rows so overlap.  The stages of consecutive tiles follow
 // each other without a gap: the next tile's operands arrive while this one's
-// last products run and its results leave (through a piece of LDS of each
-// wave's own, no barrier), which hides the output's HBM time; a block per tile
-// (with 8 waves and two barriers a stage) took 334 us for the 131072 x 1536 x
-// 2048 product of 128 experts, of which its output cost 92.
+// last products run and its results leave, through a piece of LDS of each
+// wave's own, no barrier, and past the caches (nothing here reads them again,
+// and operands stay: 310 -> 294 us).
 //
-// Scales: a thread owns SR of the stage's BM + BN rows, loads their 8 (4) bytes
-// with the DMA into registers and writes them to LDS before the barrier, in the
-// order the lanes consume them: lane (r, g) of wave row w finds the bytes of
-// its FM row blocks and both K steps side by side, so one LDS read per operand
-// and stage brings them all, and the instruction's byte select picks each one.
+// 131072 rows of 128 experts, 1536 x 2048: 294 us, 2.8 PFLOP/s; a block per
+// tile with 8 waves and two barriers a stage took 339.  One 4096 x 4096 weight
+// and 16384 rows: 148 us, 3.7 PFLOP/s.  What bounds it: 4 waves of 1 on a SIMD
+// leave what a wave waits for (DMA, LDS, barrier) in the open: products alone
+// take 123 us of the first and 70 of the second, without output 232 and 144.
+//
+// Scales: the words of a row's four K blocks come by DMA too, one K step of 64
+// rows an instruction, in LDS in the order (wave row, r, i) of row 16 i + r of
+// the wave's, so that a lane reads those of its FM fragments side by side.
+// Where K is not a multiple of 128 the words are not aligned, and they pass
+// through registers.  (16 bytes of a row at a time, four K steps, quarter the
+// requests but took longer to read from LDS: MXFP8 422 -> 440 us, MXFP4 the same.)
 // ---------------------------------------------------------------------------
 template <int N, class F, int... I>
 __device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
@@ -723,7 +684,7 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
         if constexpr (c + 1 < NC) get(std::integral_constant<int, c + 1>{});
 #pragma unroll
         for (int q = 0; q < NP; ++q)
-          *reinterpret_cast<u32x4u_t*>(o0 + (int64_t)(16 * (c / NH) + q * RPP) * a.ldc + c % NH * COLS) = v[c % 2][q];
+          __builtin_nontemporal_store(v[c % 2][q], reinterpret_cast<u32x4u_t*>(o0 + (int64_t)(16 * (c / NH) + q * RPP) * a.ldc + c % NH * COLS));
       });
     } else {
       static_for<NC>([&](auto c_) {
@@ -818,13 +779,12 @@ int64_t max_tiles(const Mx4Args& a, int bm) {
   return (a.E < a.rows ? a.E : a.rows) + (int64_t)a.rows / bm;
 }
 
-template <bool FP8, bool SC4, int MF, int KS>
+template <bool FP8, bool SC4>
 hipError_t launch_stream(const Mx4Args& a, hipStream_t s) {
-  const int cols = 16 * (4 / KS);
-  const int n_groups = (a.N + cols - 1) / cols;
-  const int64_t grid = max_tiles(a, 16 * MF) * n_groups;
+  const int n_groups = (a.N + 15) / 16;
+  const int64_t grid = max_tiles(a, 16) * n_groups;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return launch_kernel(mx4_stream_kernel<FP8, SC4, MF, KS>, dim3((unsigned)grid), dim3(256), 0, s, a, n_groups);
+  return launch_kernel(mx4_stream_kernel<FP8, SC4>, dim3((unsigned)grid), dim3(256), 0, s, a, n_groups);
 }
 
 template <class C>
@@ -840,10 +800,22 @@ template <bool FP8, bool SC4>
 hipError_t launch_formats(const Mx4Args& a, hipStream_t s) {
   // scales that pass through registers are read 8 bytes at a time: that many in each array
   const bool room = SC4 || ((int64_t)a.a_rows * a.KB >= 8 && (int64_t)a.E * a.N * a.KB >= 8);
-  if constexpr (SC4)
-    if (a.rows / a.E >= MX4_BIG) return launch_tiles<Mx4Cfg<FP8, SC4, 256, 256, 2, 2, 1>>(a, s);
-  if (room && a.rows / a.E >= MX4_MID) return launch_tiles<Mx4Cfg<FP8, SC4, 128, 128, 2, 2, 2>>(a, s);
-  return launch_stream<FP8, SC4, 1, 4>(a, s);
+  // The stream kernel reads the weights once for every 16 rows of an expert, the tile kernel needs tiles for the whole
+  // device: up to 48 MiB read so the first was faster (24 rows on 128 experts' 1536 x 2048, 36 MiB: 12.6 us against
+  // 13.6; 64 rows of one 4096 x 4096 weight: 17.3, 17.1), above it the second (48 rows of the 128: 21.4, 17.4;
+  // 1024 rows: 77.9, 36.7).
+  const int64_t streamed = max_tiles(a, 16) * a.N * a.KB * 16;
+  if (!room || streamed <= (int64_t)48 << 20) return launch_stream<FP8, SC4>(a, s);
+  if constexpr (SC4) {
+    // 256 x 256 tiles halve the operands' traffic and want few partial tiles, one for every compute unit and a K that
+    // outweighs the walk from tile to tile.  Against 128 x 128 ones: 1024 rows for each of 128 experts, 1536 x 2048:
+    // 302 us and 324 (MXFP8 436, 471), 4096 rows of one 4096 x 4096 weight 44 and 57; but for 512 rows each 177 and
+    // 173, for 256 rows 139 and 105, for 2048 rows of the one weight 39 and 33, for 1024 rows each at K = 768 209 and 205.
+    const int64_t tiles = (int64_t)(a.rows / 256) * ((a.N + 255) / 256);
+    if (a.rows / a.E >= 1024 && a.K >= 2048 && tiles >= resident_blocks(1))
+      return launch_tiles<Mx4Cfg<FP8, SC4, 256, 256, 2, 2, 1>>(a, s);
+  }
+  return launch_tiles<Mx4Cfg<FP8, SC4, 128, 128, 2, 2, 2>>(a, s);
 }
 
 }  // namespace

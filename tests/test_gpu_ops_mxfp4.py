@@ -194,8 +194,8 @@ class Product:
             mag[r] = np.abs(x[r]) @ np.abs(self.bv[e]).T
         return out, mag
 
-    def check(self, c, typ):
-        want, mag = self.reference()
+    def check(self, c, typ, ref=None):
+        want, mag = ref or self.reference()
         M = int(self.offsets[-1])
         got = c.double().cpu().numpy()
         rel = (-(-self.K // 128) + 2) * 2.0 ** -23 if self.fmt == "mxfp4" else 2e-4
@@ -220,6 +220,39 @@ CASES = [
     ([5] * 300 + [0] * 212, 33, 64, 64, 4),
     ([1024], 256, 512, None, 1),
 ]
+# long enough for the tiles through LDS: 128 x 128, then 256 x 256; K of whole and of broken steps, words and stages
+TILED = [
+    ([3000, 5100], 3201, 40, None, 1),
+    ([100] * 300 + [0] * 212, 270, 160, 64, 4),
+    ([140, 900, 0, 12, 329], 1136, 1120, 100, 6),
+    ([130, 0, 5, 64, 2700], 1500, 512, 50, 4),
+    ([1000, 24, 1], 1030, 1664, None, 1),
+    ([20] * 10, 2301, 2048, 12, 7),
+    ([257, 1], 3000, 2080, None, 1),
+    ([1700, 1, 2500], 4100, 2048, 700, 3),
+    ([4111], 4099, 2170, None, 1),
+]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("case", TILED, ids=lambda c: f"{len(c[0])}x{sum(c[0])}-{c[1]}-{c[2]}")
+def test_product_tiled(case, fmt):
+    import torch
+    import grouped_gemm_layer_amd as g
+    counts, N, K, T, k = case
+    if fmt == "mxfp8":
+        K = -(-K // 32) * 32
+    print(f"[product] {len(counts)} experts, {sum(counts)} rows, N={N} K={K} {fmt}", flush=True)
+    p = Product(counts, N, K, fmt, T, k)
+    ref = p.reference()
+    for typ in ("bf16", "fp32"):
+        c = torch.full((p.rows, N + 3), 5.0, dtype=_dt(typ), device="cuda")
+        g.mxfp4_product(*p.args, c[:, 2:2 + N], **p.kw)
+        p.check(c[:, 2:2 + N], typ, ref)
+        assert bool((c[:, :2] == 5).all()) and bool((c[:, -1:] == 5).all())
+        c2 = torch.empty(p.rows, N, dtype=_dt(typ), device="cuda")
+        g.mxfp4_product(*p.args, c2, **p.kw)
+        assert torch.equal(c2, c[:, 2:2 + N])
 
 
 @pytest.mark.parametrize("typ", ["bf16", "fp32"])
@@ -242,23 +275,25 @@ def test_product(case, fmt, typ):
     assert torch.equal(c2, c[:, 2:2 + N])                # the pitch changes nothing
 
 
-@pytest.mark.parametrize("rows", [1, 16, 200, 900])
-def test_product_without_experts(rows):
+@pytest.mark.parametrize("rows,N,K", [(1, 200, 384), (16, 200, 384), (200, 200, 384), (900, 200, 384),
+                                      (1500, 3000, 384), (4100, 4100, 2048)])
+def test_product_without_experts(rows, N, K):
     import torch
     import grouped_gemm_layer_amd as g
-    p = Product([rows], 200, 384, "mxfp4", dense=True)
-    c = torch.empty(rows, 200, device="cuda")
+    p = Product([rows], N, K, "mxfp4", dense=True)
+    c = torch.empty(rows, N, device="cuda")
     g.mxfp4_product(*p.args, c, **p.kw)
     p.check(c, "fp32")
 
 
-@pytest.mark.parametrize("counts", [[3, 0, 5], [100, 70, 0], [600, 300]])
-def test_rows_behind_the_last_stay(counts):
+@pytest.mark.parametrize("counts,N,K", [([3, 0, 5], 72, 256), ([100, 70, 0], 72, 256), ([600, 300], 72, 256),
+                                        ([100, 1900, 0], 1100, 1024), ([2500, 2000], 4100, 2048)])
+def test_rows_behind_the_last_stay(counts, N, K):
     """c longer than the rows routed: the rest is left as it was; no rows at all; offsets past c are cut."""
     import torch
     import grouped_gemm_layer_amd as g
-    p = Product(counts, 72, 256, "mxfp4", T=20, k=2, gap=37)
-    c = torch.full((p.rows, 72), 5.0, device="cuda")
+    p = Product(counts, N, K, "mxfp4", T=20, k=2, gap=37)
+    c = torch.full((p.rows, N), 5.0, device="cuda")
     g.mxfp4_product(*p.args, c, **p.kw)
     p.check(c, "fp32")
     M = sum(counts)
@@ -268,23 +303,23 @@ def test_rows_behind_the_last_stay(counts):
     assert torch.equal(c, torch.full_like(c, 5.0))
     far = p.kw["offsets"].clone()
     far[-1] += 1000
-    buf = torch.full((p.rows + 2000, 72), 5.0, device="cuda")
+    buf = torch.full((p.rows + 2000, N), 5.0, device="cuda")
     g.mxfp4_product(*p.args, buf[:p.rows], **dict(p.kw, offsets=far))
     assert torch.equal(buf[p.rows:], torch.full_like(buf[p.rows:], 5.0))
 
 
-@pytest.mark.parametrize("rows", [8, 100, 400])
+@pytest.mark.parametrize("rows,N,K", [(8, 90, 352), (100, 90, 352), (400, 90, 352), (1600, 1100, 1056), (2100, 4100, 2048)])
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
-def test_scale_255_makes_what_it_enters_nan(fmt, rows):
+def test_scale_255_makes_what_it_enters_nan(fmt, rows, N, K):
     import torch
     import grouped_gemm_layer_amd as g
-    p = Product([rows, rows], 90, 352, fmt)
+    p = Product([rows, rows], N, K, fmt)
     sa, sb = p.args[1], p.args[3]
     sa[3, 2] = 255
     sb[1, 7, 10] = 255
-    c = torch.empty(p.rows, 90, device="cuda")
+    c = torch.empty(p.rows, N, device="cuda")
     g.mxfp4_product(*p.args, c, **p.kw)
-    nan = torch.zeros(p.rows, 90, dtype=torch.bool, device="cuda")
+    nan = torch.zeros(p.rows, N, dtype=torch.bool, device="cuda")
     nan[3] = True
     nan[rows:, 7] = True
     assert torch.equal(c.isnan(), nan)
@@ -336,13 +371,14 @@ def test_large_output_offsets():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("counts", [[3, 0, 5], [100, 70, 0, 40], [300, 600]])
-def test_graph_replays_and_streams(counts):
+@pytest.mark.parametrize("counts,N,K", [([3, 0, 5], 136, 512), ([100, 70, 0, 40], 136, 512), ([300, 600], 136, 512),
+                                        ([300, 1600], 1136, 1024), ([2200, 2000], 4100, 2048)])
+def test_graph_replays_and_streams(counts, N, K):
     import torch
     import grouped_gemm_layer_amd as g
-    p = Product(counts, 136, 512, "mxfp4", T=30, k=4)
-    x = torch.randn(30, 512, device="cuda").bfloat16()
-    c = torch.empty(p.rows, 136, dtype=torch.bfloat16, device="cuda")
+    p = Product(counts, N, K, "mxfp4", T=30, k=4)
+    x = torch.randn(30, K, device="cuda").bfloat16()
+    c = torch.empty(p.rows, N, dtype=torch.bfloat16, device="cuda")
 
     def step():
         g.mxfp4_quantize(x, p.args[0], p.args[1])
