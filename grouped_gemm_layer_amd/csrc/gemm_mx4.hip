@@ -589,30 +589,34 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
         take_source(nk - (kt + 2));
         set_dma(kt + 2 < nk ? kt + 2 : kt + 2 - nk);
         if constexpr (!C::SC4) load_scales(dma_kt);
-        read_scales(st ^ 1, 0, nset);
       }
-      if constexpr (!LAST && i == 0) read_scales(st, s + 1, nset);
-      if constexpr (i + 3 < FM) read_a(st, s, i + 3, (i + 3) % 4);
-      else if constexpr (!LAST) read_a(st, s + 1, i + 3 - FM, (i + 3) % 4);
-      else read_a(st ^ 1, 0, i + 3 - FM, (i + 3) % 4);
-      if constexpr (!LAST) {
-        constexpr int per = (FN + FM - 1) / FM;
-        static_for<per>([&](auto q_) { if constexpr (i * per + q_ < FN) read_b(st, s + 1, i * per + q_, nset); });
-      } else if constexpr (i >= C::PB) {
-        constexpr int per = (FN + FM - C::PB - 1) / (FM - C::PB);
-        static_for<per>([&](auto q_) {
-          if constexpr ((i - C::PB) * per + q_ < FN) read_b(st ^ 1, 0, (i - C::PB) * per + q_, nset);
-        });
-      }
-      // the stage's DMAs, DPR a row from the barrier on; the last ones in the next stage's first unit, unless they were
-      // sent before the output
+      // What a row does beside its products goes between them, one thing after each: the row's other instructions
+      // would otherwise hold up the matrix core, which has no second wave to turn to.
       constexpr bool head = LAST && i >= C::PB;
       constexpr int at = head ? i - C::PB : s == 0 && i < C::PB_FIRST ? C::D_TAIL / C::DPR + i : -1;
-      if constexpr (at >= 0) static_for<C::DPR>([&](auto q_) {
-        constexpr int d = at * C::DPR + q_;
-        if constexpr (d < C::D) dma(std::integral_constant<int, d>{}, std::bool_constant<head>{}, head ? st : st ^ 1, kt);
-      });
-      __builtin_amdgcn_sched_barrier(0);
+      constexpr int per_b = !LAST ? (FN + FM - 1) / FM : head ? (FN + FM - C::PB - 1) / (FM - C::PB) : 0;
+      constexpr int b0 = (!LAST ? i : i - C::PB) * per_b;
+      constexpr bool scales = LAST ? i == C::PB : i == 0;
+      constexpr int acts = 1 + per_b + (at >= 0 ? C::DPR : 0) + (scales ? 1 : 0);
+      auto act = [&](auto n_) __attribute__((always_inline)) {
+        constexpr int n = n_;
+        constexpr int m = n - (scales ? 1 : 0);
+        if constexpr (scales && n == 0) {
+          if constexpr (LAST) read_scales(st ^ 1, 0, nset); else read_scales(st, s + 1, nset);
+        } else if constexpr (m == 0) {
+          if constexpr (i + 3 < FM) read_a(st, s, i + 3, (i + 3) % 4);
+          else if constexpr (!LAST) read_a(st, s + 1, i + 3 - FM, (i + 3) % 4);
+          else read_a(st ^ 1, 0, i + 3 - FM, (i + 3) % 4);
+        } else if constexpr (m <= per_b) {
+          constexpr int jb = b0 + m - 1;
+          if constexpr (jb < FN) { if constexpr (LAST) read_b(st ^ 1, 0, jb, nset); else read_b(st, s + 1, jb, nset); }
+        } else {
+          // the stage's DMAs, DPR a row from the barrier on; the last ones in the next stage's first unit, unless they
+          // were sent before the output
+          constexpr int d = at * C::DPR + m - 1 - per_b;
+          if constexpr (d < C::D) dma(std::integral_constant<int, d>{}, std::bool_constant<head>{}, head ? st : st ^ 1, kt);
+        }
+      };
       static_for<FN>([&](auto j_) {
         constexpr int j = j_;
         const u32x4_t b = br[set][j], x = ar[i % 4], h = C::FP8 ? ar_h[C::FP8 ? i % 4 : 0] : u32x4_t{0u, 0u, 0u, 0u};
@@ -623,6 +627,8 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc[i][j], FMT_FP4,
                                                                      C::FP8 ? FMT_FP8 : FMT_FP4, 0, (int)xb[set][j], 0,
                                                                      (int)xa[set][i]);
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<acts>([&](auto n_) { if constexpr (n_ * FN / acts == j) { act(n_); __builtin_amdgcn_sched_barrier(0); } });
       });
     });
   };
