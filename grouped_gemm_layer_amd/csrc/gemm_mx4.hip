@@ -207,25 +207,28 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
 // four), B's during the unit before (two sets).  Row PB of a stage's last unit,
 // where the wave's last read of the stage has been issued, is the stage's only
 // barrier: it publishes the next stage and frees this one, into which the DMA
-// of the stage after the next then runs, DPR instructions a row.  Reads, DMA
-// and products of all rows so overlap.  The stages of consecutive tiles follow
-// each other without a gap: the next tile's operands arrive while this one's
-// last products run and its results leave, through a piece of LDS of each
-// wave's own, no barrier, and past the caches (nothing here reads them again,
-// and operands stay: 310 -> 294 us).
-//
-// 131072 rows of 128 experts, 1536 x 2048: 294 us, 2.8 PFLOP/s; a block per
-// tile with 8 waves and two barriers a stage took 339.  One 4096 x 4096 weight
-// and 16384 rows: 148 us, 3.7 PFLOP/s.  What bounds it: 4 waves of 1 on a SIMD
-// leave what a wave waits for (DMA, LDS, barrier) in the open: products alone
-// take 123 us of the first and 70 of the second, without output 232 and 144.
+// of the stage after the next then runs, DPR instructions a row.  All of it
+// goes between the products, one instruction or two after each.  The stages of
+// consecutive tiles follow each other without a gap: the next tile's operands
+// arrive while this one's last products run and its results leave, through a
+// piece of LDS of each wave's own, no barrier, in whole lines (stores of 64
+// bytes of a row cost 14%) and past the caches (nothing here reads them again;
+// 310 -> 294 us).
 //
 // Scales: the words of a row's four K blocks come by DMA too, one K step of 64
-// rows an instruction, in LDS in the order (wave row, r, i) of row 16 i + r of
-// the wave's, so that a lane reads those of its FM fragments side by side.
-// Where K is not a multiple of 128 the words are not aligned, and they pass
-// through registers.  (16 bytes of a row at a time, four K steps, quarter the
-// requests but took longer to read from LDS: MXFP8 422 -> 440 us, MXFP4 the same.)
+// rows an instruction.  A lane reads one word for four fragments and gets its
+// byte of each by a 4 x 4 transpose over four lanes; the instruction's byte
+// select picks it.  Where K is not a multiple of 128 the words are not aligned,
+// and they pass through registers.  (16 bytes of a row at a time, four K steps,
+// are a quarter of the requests, but LDS then has no room for the output's
+// lines: as fast at best.)
+//
+// 131072 rows of 128 experts, 1536 x 2048: 275 us, 3.0 PFLOP/s (MXFP8 390); one
+// 4096 x 4096 weight, 16384 rows: 147 us, 3.7 PFLOP/s.  With 4 waves of 128 x
+// 128 in place of 8 of 128 x 64: 290 and 153; a block per tile and two barriers
+// a stage: 339 and 171.  What bounds it, in parts of the second: the products
+// alone 70 us (the clock falls to 1.9 GHz), the DMA alone 114, of which the
+// scales, 4 bytes of a line each, are 26; without output 143.
 // ---------------------------------------------------------------------------
 template <int N, class F, int... I>
 __device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
@@ -292,7 +295,6 @@ struct Mx4Cfg {
   static constexpr int NW = WGM * WGN, NTHR = 64 * NW;
   static constexpr int WPE = PER_CU * NW / 4;            // waves per SIMD
   static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
-  static constexpr bool ACC = FM * FN == 64;
   static constexpr int KST = FP8 ? 128 : 256;            // K per stage
   static constexpr int SS = KST / KSTEP;                 // units per stage
   static constexpr int RA = 128, RB = KST / 2;           // code bytes per row and stage
@@ -305,7 +307,7 @@ struct Mx4Cfg {
   static constexpr int DS = SC4 ? SR * SS : 0;           // 256-byte DMAs of scales per wave and stage
   static constexpr int D = DA + DB + DS;
   static constexpr int PB = FM - 3;                      // row of the barrier
-  static constexpr int DPR = 3;                          // DMAs per row of products
+  static constexpr int DPR = NW == 8 ? 2 : 3;                // DMAs per row of products
   static constexpr int D_TAIL = (FM - PB) * DPR;         // DMAs of a stage issued before the next one begins
   static constexpr int PB_FIRST = SS == 1 ? PB - 1 : FM; // rows of a stage's first unit that may issue the others
   static constexpr int OUT_ROW = WN * 2, OUT_WAVE = 16 * OUT_ROW;   // bytes of a wave's output in LDS: 16 rows
@@ -316,7 +318,7 @@ struct Mx4Cfg {
   static constexpr int LDS = ROWS0 + 2 * BM * 4;
   static_assert(DA * NW * 1024 == A_BYTES && DB * NW * 1024 == B_BYTES, "whole DMAs per wave");
   static_assert(SR * NTHR == BM + BN && BM == BN && SR <= 2, "scale rows: one of each operand per thread, or of one");
-  static_assert(FM % 4 == 0 && FN == FM && WM == WN, "whole 16-byte pieces of scales per lane");
+  static_assert(FM % 4 == 0 && FN % 4 == 0, "whole words of scales per lane");
   static_assert(PB >= 1, "ring of four A fragments");
   static_assert(D - D_TAIL <= PB_FIRST * DPR, "the other DMAs fit before the next barrier");
   static_assert(NW * OUT_WAVE >= 513 * 4, "the prefix sums fit where the output is staged");
@@ -440,7 +442,6 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
     const bool ok = t.e >= 0 && t.m0 + tid < t.mlim && map_v >= 0 && s < a.a_rows;
     if (tid < BM) s_rows[(it & 1) * BM + tid] = ok ? (uint32_t)s * pa : OOB;
   };
-  const int sc_i = ((64 * wave) & (BM - 1)) + lane, sc_at = sc_i / (16 * FM) * WM + 16 * (sc_i % FM) + sc_i / FM % 16;
   auto aim = [&](const Tile& t, int it, Source& o) __attribute__((always_inline)) {
     const uint32_t* rows = s_rows + (it & 1) * BM;
     const int64_t e = max(t.e, 0);
@@ -459,8 +460,8 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
       o.ob[i] = n < n_left ? (uint32_t)(t.n0 + n) * pb + colb : OOB;
     }
 #pragma unroll
-    for (int q = 0; q < C::SR; ++q) {                    // this lane's scale row (through a register: this thread's)
-      const int R = C::SC4 ? sc_at : sc_r(q);
+    for (int q = 0; q < C::SR; ++q) {                    // this thread's scale rows
+      const int R = sc_r(q);
       const uint32_t r = rows[R & (BM - 1)];
       const uint32_t va = r == OOB ? OOB : r >> (C::FP8 ? 5 : 4), vb = R < n_left ? (uint32_t)(t.n0 + R) * a.KB : OOB;
       o.os[q] = sc_is_b(q) ? vb : va;
@@ -531,8 +532,7 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
     for (int q = 0; q < C::SR; ++q) {
       const bool b = sc_is_b(q);
       const sc_t v = sc_fix[q] >= 8 * C::SB ? (sc_t)0 : (sc[q] >> sc_fix[q]) & sc_mask;
-      const int R = sc_r(q), at = (R / WM * 16 + R % 16) * FM + R % WM / 16;
-      uint32_t* p = reinterpret_cast<uint32_t*>(smem + st * C::STAGE + (b ? C::B_SC : C::A_SC)) + at;
+      uint32_t* p = reinterpret_cast<uint32_t*>(smem + st * C::STAGE + (b ? C::B_SC : C::A_SC)) + sc_r(q);
 #pragma unroll
       for (int s = 0; s < SS; ++s) p[s * BM] = (uint32_t)(v >> (32 * (s % SS)));
     }
@@ -541,7 +541,7 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
   // ---------------- fragments
   f32x4_t acc[FM][FN];
   u32x4_t ar[4], ar_h[C::FP8 ? 4 : 1], br[2][FN];     // (kept as the four words that MXFP4 codes take)
-  uint32_t xa[2][FM], xb[2][FN];                      // scale words, as many sets; byte g counts
+  uint32_t xa[2][FM / 4], xb[2][FN / 4];              // scales, as many sets: byte i % 4 of word i / 4
   const int sw = rl & 7;                              // rows of a fragment differ from rl by multiples of 16
   auto read_a = [&](int st, int s, int i, int slot) __attribute__((always_inline)) {
     const uint8_t* p = smem + st * C::STAGE + (wm * WM + 16 * i + rl) * 128;
@@ -554,13 +554,22 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
     if constexpr (C::RB == 128) br[set][j] = *reinterpret_cast<const u32x4_t*>(p + row * 128 + (((4 * s + g) ^ sw) << 4));
     else br[set][j] = *reinterpret_cast<const u32x4_t*>(p + (row >> 1) * 128 + ((((rl & 1) * 4 + g) ^ ((rl >> 1) & 7)) << 4));
   };
+  // Lane (r, g) fetches the word of row 16 g + r, the four K blocks of fragment g, and needs byte g of the four
+  // fragments: a 4 x 4 transpose of bytes over the four lanes of r.
   auto read_scales = [&](int st, int s, int set) __attribute__((always_inline)) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(smem + st * C::STAGE + C::A_SC) + s * BM + (wm * 16 + rl) * FM;
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(smem + st * C::STAGE + C::B_SC) + s * BN + (wn * 16 + rl) * FN;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(smem + st * C::STAGE + C::A_SC) + s * BM + wm * WM + lane;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(smem + st * C::STAGE + C::B_SC) + s * BN + wn * WN + lane;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) xa[set][i] = p[i];
+    for (int i = 0; i < FM / 4; ++i) xa[set][i] = p[64 * i];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) xb[set][j] = q[j];
+    for (int j = 0; j < FN / 4; ++j) xb[set][j] = q[64 * j];
+  };
+  const uint32_t sel_half = g & 2 ? 0x03020706u : 0x01000504u, sel_byte = g & 1 ? 0x03070105u : 0x02060004u;
+  auto turn = [&](uint32_t& x) __attribute__((always_inline)) {
+    const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);        // words of fragments g % 2 and g % 2 + 2
+    const uint32_t w = __builtin_amdgcn_perm(h[0], h[1], sel_half);             // their bytes g / 2 * 2 and the next
+    const auto q = __builtin_amdgcn_permlane16_swap(w, w, false, false);        // the same of fragments 0, 2 and 1, 3
+    x = __builtin_amdgcn_perm(q[0], q[1], sel_byte);
   };
 
   // ---------------- state of the walk
@@ -597,12 +606,15 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
       constexpr int per_b = !LAST ? (FN + FM - 1) / FM : head ? (FN + FM - C::PB - 1) / (FM - C::PB) : 0;
       constexpr int b0 = (!LAST ? i : i - C::PB) * per_b;
       constexpr bool scales = LAST ? i == C::PB : i == 0;
-      constexpr int acts = 1 + per_b + (at >= 0 ? C::DPR : 0) + (scales ? 1 : 0);
+      constexpr bool turns = i == FM - 1;             // the next unit's scales
+      constexpr int acts = 1 + per_b + (at >= 0 ? C::DPR : 0) + (scales ? 1 : 0) + (turns ? FM / 4 + FN / 4 : 0);
       auto act = [&](auto n_) __attribute__((always_inline)) {
         constexpr int n = n_;
-        constexpr int m = n - (scales ? 1 : 0);
+        constexpr int m = n - (scales ? 1 : turns ? FM / 4 + FN / 4 : 0);
         if constexpr (scales && n == 0) {
           if constexpr (LAST) read_scales(st ^ 1, 0, nset); else read_scales(st, s + 1, nset);
+        } else if constexpr (m < 0) {
+          if constexpr (n < FN / 4) turn(xb[nset][n]); else turn(xa[nset][n - FN / 4]);
         } else if constexpr (m == 0) {
           if constexpr (i + 3 < FM) read_a(st, s, i + 3, (i + 3) % 4);
           else if constexpr (!LAST) read_a(st, s + 1, i + 3 - FM, (i + 3) % 4);
@@ -622,11 +634,9 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
         const u32x4_t b = br[set][j], x = ar[i % 4], h = C::FP8 ? ar_h[C::FP8 ? i % 4 : 0] : u32x4_t{0u, 0u, 0u, 0u};
         const i32x8_t fb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
         const i32x8_t fa = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
-        if constexpr (i == 0) xb[set][j] >>= 8 * g;
-        if constexpr (j == 0) xa[set][i] >>= 8 * g;
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc[i][j], FMT_FP4,
-                                                                     C::FP8 ? FMT_FP8 : FMT_FP4, 0, (int)xb[set][j], 0,
-                                                                     (int)xa[set][i]);
+                                                                     C::FP8 ? FMT_FP8 : FMT_FP4, j % 4,
+                                                                     (int)xb[set][j / 4], i % 4, (int)xa[set][i / 4]);
         __builtin_amdgcn_sched_barrier(0);
         static_for<acts>([&](auto n_) { if constexpr (n_ * FN / acts == j) { act(n_); __builtin_amdgcn_sched_barrier(0); } });
       });
@@ -640,7 +650,9 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) br[0][j] = br[1][j];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) { xb[0][j] = xb[1][j]; xa[0][j] = xa[1][j]; }
+      for (int j = 0; j < FN / 4; ++j) xb[0][j] = xb[1][j];
+#pragma unroll
+      for (int i = 0; i < FM / 4; ++i) xa[0][i] = xa[1][i];
     }
     st ^= 1;
   };
@@ -665,7 +677,6 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
       constexpr int i = c_ / NH, h = c_ % NH;
 #pragma unroll
       for (int jj = 0; jj < COLS / 16; ++jj) {
-        if constexpr (C::ACC) asm volatile("" : "+a"(acc[i][h * (COLS / 16) + jj]));   // (not moved before their turn)
         const f32x4_t v = acc[i][h * (COLS / 16) + jj];
         const int byte = (16 * jj + 4 * g) * (int)sizeof(T);
         uint8_t* p = stg + rl * C::OUT_ROW + (((byte >> 4) ^ (rl % NQ)) << 4) + (byte & 15);
@@ -740,6 +751,10 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
   __syncthreads();
   read_scales(0, 0, 0);
 #pragma unroll
+  for (int i = 0; i < FM / 4; ++i) turn(xa[0][i]);
+#pragma unroll
+  for (int j = 0; j < FN / 4; ++j) turn(xb[0][j]);
+#pragma unroll
   for (int j = 0; j < FN; ++j) read_b(0, 0, j, 0);
   read_a(0, 0, 0, 0);
   read_a(0, 0, 1, 1);
@@ -753,12 +768,7 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        // 64 fragments fill the accumulation registers to the last one: named here as their place, or the
-        // compiler deals them over both kinds of registers and moves hundreds in every stage
-        if constexpr (C::ACC) asm volatile("" : "+a"(acc[i][j]));
-      }
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma nounroll
     for (kt = 0; kt < nk; ++kt) stage();
     send(rest, st ^ 1);           // the rest of the next tile's second stage, ahead of the stores
@@ -819,7 +829,7 @@ hipError_t launch_formats(const Mx4Args& a, hipStream_t s) {
     // 173, for 256 rows 139 and 105, for 2048 rows of the one weight 39 and 33, for 1024 rows each at K = 768 209 and 205.
     const int64_t tiles = (int64_t)(a.rows / 256) * ((a.N + 255) / 256);
     if (a.rows / a.E >= 1024 && a.K >= 2048 && tiles >= resident_blocks(1))
-      return launch_tiles<Mx4Cfg<FP8, SC4, 256, 256, 2, 2, 1>>(a, s);
+      return launch_tiles<Mx4Cfg<FP8, SC4, 256, 256, 2, 4, 1>>(a, s);
   }
   return launch_tiles<Mx4Cfg<FP8, SC4, 128, 128, 2, 2, 2>>(a, s);
 }
