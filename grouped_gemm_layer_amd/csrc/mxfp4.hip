@@ -31,8 +31,14 @@ __device__ __forceinline__ float mx4_scale(uint32_t s) {
 }
 constexpr uint32_t NONFINITE = 0x7F800000u;
 
-// 8 values -> 8 codes in one word (value i in bits 4i .. 4i+3)
-__device__ __forceinline__ uint32_t mx4_pack8(const float (&v)[8], float inv) {
+// 8 values -> 8 codes in one word (value i in bits 4i .. 4i+3); 4 values -> the low half of one
+__device__ __forceinline__ uint32_t mx4_pack(const float (&v)[4], float inv) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * inv, v[1] * inv, 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * inv, v[3] * inv, 1.0f, 1);
+  return w;
+}
+__device__ __forceinline__ uint32_t mx4_pack(const float (&v)[8], float inv) {
   uint32_t w = 0;
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * inv, v[1] * inv, 1.0f, 0);
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * inv, v[3] * inv, 1.0f, 1);
@@ -41,53 +47,57 @@ __device__ __forceinline__ uint32_t mx4_pack8(const float (&v)[8], float inv) {
   return w;
 }
 
-// 8 consecutive values of a row, n of them inside (zeros behind)
-__device__ __forceinline__ void load8(const bf16_t* p, int n, float (&v)[8]) {
-  RowVec<bf16_t>::load_once(p, n).unpack(v);
-}
-__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
-  float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-  RowVec<float>::load_once(p, min(n, 4)).unpack(a);
-  if (n > 4) RowVec<float>::load_once(p + 4, n - 4).unpack(b);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
-}
+// Along the rows a lane handles 16 bytes of values, 8 of bf16 or 4 of fp32, and
+// the codes of those: 4 or 8 lanes a block, so that a wave's loads and stores
+// are consecutive bytes on both sides.  (With 8 fp32 values a lane, in two
+// pieces, the way back to 131072 x 2048 values took 536 us for 1.2 GB.)
+template <typename T>
+struct Lanes {
+  static constexpr int V = RowVec<T>::N, N = 32 / V, BLOCKS = 256 / N;   // values a lane, lanes a block, blocks
+  using codes_t = std::conditional_t<V == 8, uint32_t, uint16_t>;
+};
 
-// Blocks along the rows: 4 lanes per block, 8 values each, so that a wave reads
-// and writes consecutive bytes; the block maximum crosses the 4 lanes by two
-// quad swaps.  SWIGLU: v = SiLU(g1) * g3 with g1 at column c, g3 at cols + c.
+// The block maximum crosses the lanes by swaps within quads and, for eight of
+// them, the mirror of eight.  SWIGLU: v = SiLU(g1) * g3 with g1 at column c, g3
+// at cols + c.  131072 x 2048: bf16 112 us (6.0 TB/s), fp32 203 (6.0); SwiGLU of
+// them 94 (6.4) and 184 (6.2).
 template <typename T, bool SWIGLU>
 __global__ __launch_bounds__(256) void mx4_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t rows, int cols,
                                                        int kb, uint8_t* __restrict__ codes,
                                                        uint8_t* __restrict__ scales) {
-  const int q = threadIdx.x & 3;
+  using L = Lanes<T>;
+  constexpr int V = L::V;
+  const int q = threadIdx.x % L::N;
   const int64_t total = rows * kb;
-  const int64_t step = (int64_t)gridDim.x * 64;
-  for (int64_t b = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2); b < total; b += step) {   // whole quads
+  const int64_t step = (int64_t)gridDim.x * L::BLOCKS;
+  for (int64_t b = (int64_t)blockIdx.x * L::BLOCKS + threadIdx.x / L::N; b < total; b += step) {   // a block's lanes together
     const int64_t r = b / kb;
-    const int c = (int)(b - r * kb) * 32 + 8 * q;
-    const int n = min(8, cols - c);
-    float v[8];
+    const int c = (int)(b - r * kb) * 32 + V * q;
+    const int n = min(V, cols - c);
+    float v[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
     if (n > 0) {
-      load8(src + r * ld + c, n, v);
+      RowVec<T>::load_once(src + r * ld + c, n).unpack(v);
       if constexpr (SWIGLU) {
-        float g3[8];
-        load8(src + r * ld + cols + c, n, g3);
+        float g3[V];
+        RowVec<T>::load_once(src + r * ld + cols + c, n).unpack(g3);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? v[i] * sigmoid_f32(v[i]) * g3[i] : 0.f;
+        for (int i = 0; i < V; ++i) v[i] = i < n ? v[i] * sigmoid_f32(v[i]) * g3[i] : 0.f;
       }
     }
     uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < V; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     amax = max(amax, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)amax, 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
     amax = max(amax, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)amax, 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
+    if constexpr (L::N == 8)
+      amax = max(amax, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)amax, 0x141, 0xF, 0xF, false));   // row_half_mirror
     const bool bad = amax >= NONFINITE;
     const uint32_t s = mx4_scale_byte(bad ? 0u : amax);
-    const uint32_t w = mx4_pack8(v, mx4_inv_scale(s));
-    reinterpret_cast<uint32_t*>(codes)[b * 4 + q] = bad ? 0u : w;
+    const uint32_t w = mx4_pack(v, mx4_inv_scale(s));
+    using codes_t = typename L::codes_t;
+    __builtin_nontemporal_store((codes_t)(bad ? 0u : w), reinterpret_cast<codes_t*>(codes) + b * L::N + q);
     if (q == 0) scales[b] = (uint8_t)(bad ? 255u : s);
   }
 }
@@ -161,7 +171,7 @@ __global__ __launch_bounds__(256) void mx4_cols_kernel(const T* __restrict__ src
           float x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = v[c][8 * g + i];
-          w[g] = bad ? 0u : mx4_pack8(x, inv);
+          w[g] = bad ? 0u : mx4_pack(x, inv);
         }
         *reinterpret_cast<u32x4v_t*>(&s_codes[(2 * lane + c) * CODE_LD + 16 * blk]) = w;
         s_scales[(2 * lane + c) * (TR / 32) + blk] = (uint8_t)(bad ? 255u : s);
@@ -191,41 +201,41 @@ __global__ __launch_bounds__(256) void mx4_cols_kernel(const T* __restrict__ src
   }
 }
 
-// 8 codes per lane (4 bytes in, 16 or 32 out): consecutive bytes on both sides
+// The way back, lanes as along the rows.  131072 x 2048: bf16 93 us (7.3 TB/s),
+// fp32 160 (7.6).
 template <typename T>
 __global__ __launch_bounds__(256) void mx4_values_kernel(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scales, int64_t rows, int cols,
                                                          int kb, T* __restrict__ out, int64_t ld) {
-  const int q = threadIdx.x & 3;
-  const int64_t total = rows * kb, step = (int64_t)gridDim.x * 64;
-  for (int64_t b = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2); b < total; b += step) {
+  using L = Lanes<T>;
+  constexpr int V = L::V;
+  const int q = threadIdx.x % L::N;
+  const int64_t total = rows * kb, step = (int64_t)gridDim.x * L::BLOCKS;
+  for (int64_t b = (int64_t)blockIdx.x * L::BLOCKS + threadIdx.x / L::N; b < total; b += step) {
     const int64_t r = b / kb;
-    const int c = (int)(b - r * kb) * 32 + 8 * q;
-    const int n = min(8, cols - c);
-    const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[b * 4 + q];
+    const int c = (int)(b - r * kb) * 32 + V * q;
+    const int n = min(V, cols - c);
+    const uint32_t w = reinterpret_cast<const typename L::codes_t*>(codes)[b * L::N + q];
     const float s = mx4_scale(scales[b]);
     if (n <= 0) continue;
-    float v[8];
+    float v[V];
     const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
     const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
     v[0] = p0[0] * s; v[1] = p0[1] * s; v[2] = p1[0] * s; v[3] = p1[1] * s;
-    v[4] = p2[0] * s; v[5] = p2[1] * s; v[6] = p3[0] * s; v[7] = p3[1] * s;
-    T* o = out + r * ld + c;
-    if constexpr (sizeof(T) == 2) {
-      RowVec<bf16_t>::pack(v).store_once(o, n);
-    } else {
-      const float a[4] = {v[0], v[1], v[2], v[3]}, d[4] = {v[4], v[5], v[6], v[7]};
-      RowVec<float>::pack(a).store_once(o, min(n, 4));
-      if (n > 4) RowVec<float>::pack(d).store_once(o + 4, n - 4);
+    if constexpr (V == 8) {
+      const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+      const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+      v[4] = p2[0] * s; v[5] = p2[1] * s; v[6] = p3[0] * s; v[7] = p3[1] * s;
     }
+    RowVec<T>::pack(v).store_once(out + r * ld + c, n);
   }
 }
 
-// Grid of a kernel that loops over units of 64 blocks: a unit each up to 2^16
-// thread blocks (more only adds launch work), then several each.
-unsigned stream_grid(int64_t units) { return (unsigned)(units < 65536 ? units : 65536); }
+// Grid of a kernel that loops over units: a unit each up to `most` thread blocks, then several each.  Quantising
+// 131072 x 2048 fp32 values along the rows took 203 us with 2^16 blocks and 220 with one for every unit, the way back
+// 181 and 160.
+unsigned stream_grid(int64_t units, int64_t most = 65536) { return (unsigned)(units < most ? units : most); }
+constexpr int64_t EVERY_UNIT = 1 << 23;   // a launch has fewer than 2^32 threads
 
 template <typename T>
 hipError_t quantize_t(const T* src, int64_t ld, int batch, int rows, int cols, int along, int swiglu, uint8_t* codes,
@@ -233,7 +243,7 @@ hipError_t quantize_t(const T* src, int64_t ld, int batch, int rows, int cols, i
   if (along == 1) {
     const int kb = (cols + 31) / 32;
     const int64_t n = (int64_t)batch * rows;
-    const dim3 grid(stream_grid((n * kb + 63) / 64));
+    const dim3 grid(stream_grid((n * kb + Lanes<T>::BLOCKS - 1) / Lanes<T>::BLOCKS));
     return swiglu ? launch_kernel(mx4_rows_kernel<T, true>, grid, dim3(256), 0, s, src, ld, n, cols, kb, codes, scales)
                   : launch_kernel(mx4_rows_kernel<T, false>, grid, dim3(256), 0, s, src, ld, n, cols, kb, codes,
                                   scales);
@@ -254,12 +264,14 @@ hipError_t launch_mx4_quantize(const void* src, int64_t ld, int batch, int rows,
 
 hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int cols, void* out,
                                  int64_t ld, int type, hipStream_t s) {
-  const int kb = (cols + 31) / 32;
-  const dim3 grid(stream_grid(((int64_t)rows * kb + 63) / 64));
-  return type == 0 ? launch_kernel(mx4_values_kernel<float>, grid, dim3(256), 0, s, codes, scales, (int64_t)rows, cols,
-                                   kb, static_cast<float*>(out), ld)
-                   : launch_kernel(mx4_values_kernel<bf16_t>, grid, dim3(256), 0, s, codes, scales, (int64_t)rows,
-                                   cols, kb, static_cast<bf16_t*>(out), ld);
+  auto go = [&](auto zero) {
+    using T = decltype(zero);
+    const int kb = (cols + 31) / 32;
+    const int64_t units = ((int64_t)rows * kb + Lanes<T>::BLOCKS - 1) / Lanes<T>::BLOCKS;
+    return launch_kernel(mx4_values_kernel<T>, dim3(stream_grid(units, EVERY_UNIT)), dim3(256), 0, s, codes, scales,
+                         (int64_t)rows, cols, kb, static_cast<T*>(out), ld);
+  };
+  return type == 0 ? go(float{}) : go(bf16_t{});
 }
 
 }  // namespace moe
