@@ -115,19 +115,23 @@ __device__ __forceinline__ void store4(const Mx4Args& a, int m, int n, f32x4_t v
 
 // ---------------------------------------------------------------------------
 // Few rows per expert: the weights go straight into registers (each byte has
-// one reader, so LDS would only add a stop).  A block takes 16 rows and 16
+// one reader, so LDS would only add a stop).  A block takes 16 rows and CF x 16
 // columns; its four waves split K, so that even one expert's weights are read
 // by many waves, and their sums are added in wave order through LDS.
 // SC4: KB % 4 == 0, a K step's four scale bytes of a row are one aligned word.
+//
+// Bound by the latency of what a wave reads one after the other (offsets, row
+// map, operands) and by HBM: 32 rows on as many experts' 1536 x 2048, 50 MB:
+// 13.4 us, of which launching takes 2.
 // ---------------------------------------------------------------------------
-template <bool FP8, bool SC4>
+template <bool FP8, bool SC4, int CF>
 __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups) {
   constexpr int NW = 4;
   constexpr int U = 4;                         // K steps whose loads are in flight together
-  __shared__ f32x4_t s_acc[NW - 1][64];
+  __shared__ f32x4_t s_acc[NW][CF][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, rl = lane & 15;
-  const int tile = blockIdx.x / n_groups, n0 = blockIdx.x % n_groups * 16;
+  const int tile = blockIdx.x / n_groups, n0 = blockIdx.x % n_groups * (16 * CF);
   int e, m0, mlim;
   if (!find_tile(a, 16, lane, tile, e, m0, mlim)) return;
   const uint32_t pb = (uint32_t)a.KB * 16, pa = FP8 ? (uint32_t)a.K : pb;   // code bytes of a row
@@ -135,13 +139,13 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
   const auto rsb = make_rsrc(a.sb + (size_t)e * a.N * a.KB, (uint32_t)a.N * a.KB);
   const auto ra = make_rsrc(a.a, (uint32_t)a.a_rows * pa);
   const auto rsa = make_rsrc(a.sa, (uint32_t)a.a_rows * a.KB);
-  const int nb = n0 + rl, m = m0 + rl;
-  const bool nok = nb < a.N;
-  const uint32_t ob = nok ? (uint32_t)nb * pb : 0, osb = nok ? (uint32_t)nb * a.KB : 0;
+  const int m = m0 + rl;
   const int row = m < mlim ? a_row(a, m) : -1;
   const bool mok = row >= 0;
   const uint32_t oa = mok ? (uint32_t)row * pa : 0, osa = mok ? (uint32_t)row * a.KB : 0;
-  f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[CF];
+#pragma unroll
+  for (int c = 0; c < CF; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int nk = (a.K + KSTEP - 1) / KSTEP;
   const int per = (nk + NW - 1) / NW;
   const int k0 = wave * per, k1 = min(nk, k0 + per);
@@ -150,15 +154,19 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
     else return __builtin_amdgcn_raw_buffer_load_b8(r, ok && 4 * kt + g < a.KB ? row + 4 * kt + g : OOB, 0, 0);
   };
   for (int kt0 = k0; kt0 < k1; kt0 += U) {
-    u32x4_t cb[U], ca[U], cah[U];
-    int sb[U], sa[U];
+    u32x4_t cb[CF][U], ca[U], cah[U];
+    int sb[CF][U], sa[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kt = kt0 + u;
-      const uint32_t kb = (uint32_t)kt * 64 + 16 * g;
-      const bool in = kt < k1;
-      cb[u] = __builtin_amdgcn_raw_buffer_load_b128(rb, in && nok && kb < pb ? ob + kb : OOB, 0, 0);
-      sb[u] = scale(rsb, osb, in && nok, kt);
+    for (int c = 0; c < CF; ++c) {
+      const int n = n0 + 16 * c + rl;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kt = kt0 + u;
+        const uint32_t kb = (uint32_t)kt * 64 + 16 * g;
+        const bool in = kt < k1 && n < a.N;
+        cb[c][u] = __builtin_amdgcn_raw_buffer_load_b128(rb, in && kb < pb ? (uint32_t)n * pb + kb : OOB, 0, 0);
+        sb[c][u] = scale(rsb, (uint32_t)n * a.KB, in, kt);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -174,20 +182,28 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const i32x8_t fb = {(int)cb[u][0], (int)cb[u][1], (int)cb[u][2], (int)cb[u][3], 0, 0, 0, 0};
       const i32x8_t fa = {(int)ca[u][0], (int)ca[u][1], (int)ca[u][2], (int)ca[u][3],
                           (int)cah[u][0], (int)cah[u][1], (int)cah[u][2], (int)cah[u][3]};
-      const int xb = SC4 ? (int)((uint32_t)sb[u] >> (8 * g)) : sb[u], xa = SC4 ? (int)((uint32_t)sa[u] >> (8 * g)) : sa[u];
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc, FMT_FP4, FP8 ? FMT_FP8 : FMT_FP4, 0, xb, 0, xa);
+      const int xa = SC4 ? (int)((uint32_t)sa[u] >> (8 * g)) : sa[u];
+#pragma unroll
+      for (int c = 0; c < CF; ++c) {
+        const i32x8_t fb = {(int)cb[c][u][0], (int)cb[c][u][1], (int)cb[c][u][2], (int)cb[c][u][3], 0, 0, 0, 0};
+        const int xb = SC4 ? (int)((uint32_t)sb[c][u] >> (8 * g)) : sb[c][u];
+        acc[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc[c], FMT_FP4, FP8 ? FMT_FP8 : FMT_FP4, 0,
+                                                                  xb, 0, xa);
+      }
     }
   }
-  if (wave > 0) s_acc[wave - 1][lane] = acc;
-  __syncthreads();
-  if (wave > 0) return;
+  static_assert(CF <= NW, "a wave for the sums of each fragment");
 #pragma unroll
-  for (int w = 0; w < NW - 1; ++w) acc += s_acc[w][lane];
-  const int n = n0 + 4 * g;
-  if (m < mlim && n < a.N) store4(a, m, n, acc);
+  for (int c = 0; c < CF; ++c) s_acc[wave][c][lane] = acc[c];
+  __syncthreads();
+  if (wave >= CF) return;
+  f32x4_t sum = s_acc[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) sum += s_acc[w][wave][lane];
+  const int n = n0 + 16 * wave + 4 * g;
+  if (m < mlim && n < a.N) store4(a, m, n, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -795,12 +811,12 @@ int64_t max_tiles(const Mx4Args& a, int bm) {
   return (a.E < a.rows ? a.E : a.rows) + (int64_t)a.rows / bm;
 }
 
-template <bool FP8, bool SC4>
+template <bool FP8, bool SC4, int CF>
 hipError_t launch_stream(const Mx4Args& a, hipStream_t s) {
-  const int n_groups = (a.N + 15) / 16;
+  const int n_groups = (a.N + 16 * CF - 1) / (16 * CF);
   const int64_t grid = max_tiles(a, 16) * n_groups;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return launch_kernel(mx4_stream_kernel<FP8, SC4>, dim3((unsigned)grid), dim3(256), 0, s, a, n_groups);
+  if (grid >= 1 << 24) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads
+  return launch_kernel(mx4_stream_kernel<FP8, SC4, CF>, dim3((unsigned)grid), dim3(256), 0, s, a, n_groups);
 }
 
 template <class C>
@@ -817,11 +833,14 @@ hipError_t launch_formats(const Mx4Args& a, hipStream_t s) {
   // scales that pass through registers are read 8 bytes at a time: that many in each array
   const bool room = SC4 || ((int64_t)a.a_rows * a.KB >= 8 && (int64_t)a.E * a.N * a.KB >= 8);
   // The stream kernel reads the weights once for every 16 rows of an expert, the tile kernel needs tiles for the whole
-  // device: up to 48 MiB read so the first was faster (24 rows on 128 experts' 1536 x 2048, 36 MiB: 12.6 us against
-  // 13.6; 64 rows of one 4096 x 4096 weight: 17.3, 17.1), above it the second (48 rows of the 128: 21.4, 17.4;
-  // 1024 rows: 77.9, 36.7).
+  // device: up to 64 MiB read so the first is faster (32 rows on 32 experts' 1536 x 2048, 50 MB: 13.4 us against 17.5;
+  // 64 rows of one 4096 x 4096 weight, 34 MB: 13.6, 16.9), above it the second (48 rows on 48 experts, 80 MB: 18.9,
+  // 18.1; 128 rows of the one weight, 75 MB: 24.1, 16.6).  Four fragments of columns to a wave read A less often, two
+  // have more blocks: with up to 3 K steps a wave 64 tokens on 48 experts' 1000 x 1120 took 9.1 and 10.0 us, 16 tokens
+  // on 8 experts' 4096 x 1536 9.0 and 10.1; with 4 the 32 rows above 15.1 and 13.4.  (One fragment: 16.3.)
   const int64_t streamed = max_tiles(a, 16) * a.N * a.KB * 16;
-  if (!room || streamed <= (int64_t)48 << 20) return launch_stream<FP8, SC4>(a, s);
+  if (!room || streamed <= (int64_t)64 << 20)
+    return a.K <= 3 * 4 * KSTEP ? launch_stream<FP8, SC4, 4>(a, s) : launch_stream<FP8, SC4, 2>(a, s);
   if constexpr (SC4) {
     // 256 x 256 tiles halve the operands' traffic and want few partial tiles, one for every compute unit and a K that
     // outweighs the walk from tile to tile.  Against 128 x 128 ones: 1024 rows for each of 128 experts, 1536 x 2048:

@@ -219,16 +219,18 @@ CASES = [
     ([300, 256, 700], 520, 544, 400, 2),
     ([5] * 300 + [0] * 212, 33, 64, 64, 4),
     ([1024], 256, 512, None, 1),
+    ([5, 0, 17, 1], 50, 1632, 9, 3),
+    ([3, 30], 33, 4128, None, 1),
 ]
 # long enough for the tiles through LDS: 128 x 128, then 256 x 256; K of whole and of broken steps, words and stages
 TILED = [
-    ([3000, 5100], 3201, 40, None, 1),
-    ([100] * 300 + [0] * 212, 270, 160, 64, 4),
-    ([140, 900, 0, 12, 329], 1136, 1120, 100, 6),
+    ([3000, 5100], 4200, 40, None, 1),
+    ([100] * 300 + [0] * 212, 360, 160, 64, 4),
+    ([140, 900, 0, 12, 329], 1336, 1120, 100, 6),
     ([130, 0, 5, 64, 2700], 1500, 512, 50, 4),
-    ([1000, 24, 1], 1030, 1664, None, 1),
-    ([20] * 10, 2301, 2048, 12, 7),
-    ([257, 1], 3000, 2080, None, 1),
+    ([1000, 24, 1], 1230, 1664, None, 1),
+    ([28] * 10, 2451, 2048, 12, 7),
+    ([257, 1], 3601, 2080, None, 1),
     ([1700, 1, 2500], 4100, 2048, 700, 3),
     ([4111], 4099, 2170, None, 1),
 ]
@@ -276,7 +278,7 @@ def test_product(case, fmt, typ):
 
 
 @pytest.mark.parametrize("rows,N,K", [(1, 200, 384), (16, 200, 384), (200, 200, 384), (900, 200, 384),
-                                      (1500, 3000, 384), (4100, 4100, 2048)])
+                                      (1500, 3800, 384), (4100, 4100, 2048)])
 def test_product_without_experts(rows, N, K):
     import torch
     import grouped_gemm_layer_amd as g
