@@ -360,7 +360,8 @@ int32_t moe_wgrad_chunk_rows(void);
  * aligned), and 2-D operands have a row pitch `ld` in elements (>= the row
  * length); offsets are computed in 64 bits, so no operand is limited to 2 GiB
  * unless stated; a size of zero (no tokens, no rows, no tensors) is valid and
- * returns MOE_OK.  `type` is a moe_type. */
+ * returns MOE_OK; outputs overlap neither inputs nor each other, but for
+ * clipping in place.  `type` is a moe_type. */
 typedef enum {
   MOE_TYPE_FP32 = 0,
   MOE_TYPE_BF16 = 1

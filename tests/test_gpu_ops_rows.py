@@ -321,6 +321,30 @@ def test_offsets_past_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_more_tokens_than_a_launch_takes():
+    """2^22 tokens a launch: those behind get the same."""
+    import torch
+    import grouped_gemm_layer_amd as g
+    T, k, H, E = 2 ** 22 + 4099, 2, 9, 5
+    idx = torch.randint(-1, E, (T, k), dtype=torch.int32)
+    r = gpu_sort(idx.numpy(), E)
+    x, w = torch.randn(T, H, device="cuda"), torch.rand(T, k, device="cuda")
+    n = int(r.offsets[-1])
+    xp = torch.full((T * k, H), 7.0, device="cuda")
+    g.permute(x, r, xp, weights=w)
+    f = r.sorted_to_flat[:n].long()
+    assert torch.equal(xp[:n], w.view(-1)[f, None] * x[f // k]) and bool((xp[n:] == 7).all())
+    y, dw = torch.empty_like(x), torch.empty(T, k, device="cuda")
+    g.permute_backward(xp, r, y, weights=w, x=x, dweights=dw)
+    rows = torch.where((r.flat_to_sorted >= 0)[:, None], xp[r.flat_to_sorted.clamp(min=0).long()], 0.0).view(T, k, H).double()
+    want = (w[..., None] * rows).sum(1)
+    assert bool(((y - want).abs() <= 4 * U32 * (w[..., None] * rows).abs().sum(1)).all())
+    want, mag = (x[:, None] * rows).sum(2), (x[:, None] * rows).abs().sum(2)
+    assert bool(((dw - want).abs() <= (H + 2) * U32 * mag).all())
+    del x, w, xp, y, rows, want, mag
+    torch.cuda.empty_cache()
+
+
 def test_no_tokens():
     import torch
     import grouped_gemm_layer_amd as g
