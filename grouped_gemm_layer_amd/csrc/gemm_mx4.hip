@@ -331,13 +331,14 @@ struct Mx4Cfg {
   static constexpr int OUT_STORES = WM * WN * 2 / 1024;
   static constexpr int TILES = 64;                       // tiles listed at a time
   static constexpr int OUT0 = 2 * STAGE, LIST0 = OUT0 + NW * OUT_WAVE, ROWS0 = LIST0 + TILES * 16;
-  static constexpr int LDS = ROWS0 + 2 * BM * 4;
+  static constexpr int MAP0 = ROWS0 + 2 * BM * 4;
+  static constexpr int LDS = MAP0 + BM * 4;
   static_assert(DA * NW * 1024 == A_BYTES && DB * NW * 1024 == B_BYTES, "whole DMAs per wave");
   static_assert(SR * NTHR == BM + BN && BM == BN && SR <= 2, "scale rows: one of each operand per thread, or of one");
   static_assert(FM % 4 == 0 && FN % 4 == 0, "whole words of scales per lane");
   static_assert(PB >= 1, "ring of four A fragments");
   static_assert(D - D_TAIL <= PB_FIRST * DPR, "the other DMAs fit before the next barrier");
-  static_assert(NW * OUT_WAVE >= 513 * 4, "the prefix sums fit where the output is staged");
+  static_assert(NW * OUT_WAVE >= 1025 * 4, "the prefix sums and first rows fit where the output is staged");
   static_assert(LDS * PER_CU <= 160 * 1024, "LDS of a compute unit");
 };
 
@@ -356,6 +357,7 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
   // counted from the offsets, cut to [0, rows] so that no index leaves c.
   int4* const s_list = reinterpret_cast<int4*>(smem + C::LIST0);
   int* const s_pre = reinterpret_cast<int*>(smem + C::OUT0);   // tiles of the experts up to each one
+  int* const s_first = s_pre + 512;                            // their first rows, and the last one's end
   auto row_at = [&](int e) { return min(max(a.offsets[e], 0), a.rows); };
   auto list_tiles = [&](int it0) {
     int total;
@@ -363,7 +365,12 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
     if (a.offsets) {
       for (int e = tid; e < 512; e += C::NTHR) {
         int n = 0;
-        if (e < a.E) n = max(0, row_at(e + 1) - row_at(e) + BM - 1) / BM;
+        if (e < a.E) {
+          const int first = row_at(e), end = row_at(e + 1);
+          n = max(0, end - first + BM - 1) / BM;
+          s_first[e] = first;
+          if (e == a.E - 1) s_first[a.E] = end;
+        }
         s_pre[e] = n;
       }
       __syncthreads();
@@ -401,8 +408,8 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
             if (s_pre[mid] > i) hi = mid; else lo = mid + 1;
           }
           t.x = lo;
-          t.y = row_at(lo) + (i - (lo > 0 ? s_pre[lo - 1] : 0)) * BM;
-          t.z = row_at(lo + 1);
+          t.y = s_first[lo] + (i - (lo > 0 ? s_pre[lo - 1] : 0)) * BM;
+          t.z = s_first[lo + 1];
         } else {
           t.x = 0;
           t.y = i * BM;
@@ -448,15 +455,20 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
     uint32_t oa[C::DA], ob[C::DB], os[C::SR];
   };
   uint32_t* const s_rows = reinterpret_cast<uint32_t*>(smem + C::ROWS0);
-  int map_v;                          // row_map entry of this thread's row of a tile
-  auto fetch_row = [&](const Tile& t) __attribute__((always_inline)) {
-    const int m = min(t.m0 + tid, max(t.mlim - 1, 0));
-    map_v = a.row_map ? a.row_map[m] : m;
-  };
-  auto put_row = [&](const Tile& t, int it) __attribute__((always_inline)) {
-    const int s = a.row_map ? div_by((uint32_t)map_v, a.div_mul, a.div_shift) : map_v;
-    const bool ok = t.e >= 0 && t.m0 + tid < t.mlim && map_v >= 0 && s < a.a_rows;
+  auto put_row = [&](const Tile& t, int it, int v) __attribute__((always_inline)) {   // v: the row's row_map entry
+    const int s = a.row_map ? div_by((uint32_t)v, a.div_mul, a.div_shift) : t.m0 + tid;
+    const bool ok = t.e >= 0 && t.m0 + tid < t.mlim && (v >= 0 || !a.row_map) && s < a.a_rows;
     if (tid < BM) s_rows[(it & 1) * BM + tid] = ok ? (uint32_t)s * pa : OOB;
+  };
+  auto map_now = [&](const Tile& t) __attribute__((always_inline)) {
+    return a.row_map ? a.row_map[min(t.m0 + tid, max(t.mlim - 1, 0))] : 0;
+  };
+  // the entries of a later tile, to LDS: a register would have to wait for the operands on their way before it
+  const int* const s_map = reinterpret_cast<const int*>(smem + C::MAP0);
+  auto fetch_map = [&](const Tile& t) __attribute__((always_inline)) {
+    if (a.row_map && wave * 64 < BM)
+      dma_to<4, C::MAP0>(make_rsrc(a.row_map + t.m0, __builtin_amdgcn_readfirstlane(min(max(t.mlim - t.m0, 0), BM) * 4)), tid * 4, 0,
+                         __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(const __attribute__((address_space(3))) void*)smem + wave * 256));
   };
   auto aim = [&](const Tile& t, int it, Source& o) __attribute__((always_inline)) {
     const uint32_t* rows = s_rows + (it & 1) * BM;
@@ -747,11 +759,10 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
   };
   constexpr std::integral_constant<int, 0> all{};
   constexpr std::integral_constant<int, C::D_TAIL> rest{};
-  fetch_row(cur);
-  put_row(cur, 0);
-  fetch_row(nxt);
-  put_row(nxt, 1);
-  fetch_row(nxt2);
+  const int v_cur = map_now(cur), v_nxt = map_now(nxt);
+  put_row(cur, 0, v_cur);
+  put_row(nxt, 1, v_nxt);
+  fetch_map(nxt2);
   __syncthreads();
   aim(cur, 0, src);
   if constexpr (!C::SC4) {
@@ -778,9 +789,10 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
   for (;;) {
     if ((it + 3) % C::TILES == 0) list_tiles(it + 3);   // (the waves' staged output has been read by then)
     aim(nxt, it + 1, src_n);
-    put_row(nxt2, it + 2);
+    put_row(nxt2, it + 2, s_map[tid & (BM - 1)]);
     const Tile nxt3 = tile_at(it + 3);
-    fetch_row(nxt3);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the entries have been read
+    fetch_map(nxt3);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
