@@ -198,13 +198,13 @@ moe_status check_tensors(const moe_tensor* t, int32_t count, bool written) {
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].n < 0 || t[i].n > ((int64_t)1 << 40)) return MOE_ERR_DIMS;
     total += t[i].n;
+    if (total > ((int64_t)1 << 40)) return MOE_ERR_DIMS;   // (the kernels count chunks of them in 32 bits)
     if (!type_ok(t[i].type)) return MOE_ERR_UNSUPPORTED;
     if (t[i].n == 0) continue;
     if (!t[i].data) return MOE_ERR_NULL;
     if (!aligned_to(t[i].data, type_size(t[i].type)) || !aligned_to(t[i].out, type_size(t[i].type)))
       return MOE_ERR_ALIGN;
   }
-  if (total > ((int64_t)1 << 40)) return MOE_ERR_DIMS;   // (the kernels count chunks of them in 32 bits)
   if (!written) return MOE_OK;
   // byte ranges of the gradients, and of outputs elsewhere: no two may overlap
   struct Range { uintptr_t lo, hi; };
