@@ -23,70 +23,71 @@ typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 constexpr int KSTEP = 128;   // K of one scaled MFMA
 constexpr int FMT_FP8 = 0, FMT_FP4 = 4;   // format fields of the instruction
 
-// Row tile i (of height bm, counted over the experts in order) -> expert and
-// rows [m0, mlim).  Every wave finds it by itself: lane l counts the tiles of
-// experts l*per .. of the offsets, a prefix sum over the lanes and a ballot
-// give the lane that holds tile i.  That takes about 0.5 us of a tile's time
-// and saves the launch that would build a table.  Offsets are cut to [0, rows]
-// so that no index leaves c.  False when i is no tile.
-__device__ __forceinline__ bool find_tile(const Mx4Args& a, int bm, int lane, int i, int& e, int& m0, int& mlim) {
+// Row tile i (of 16 rows, counted over the experts in order) -> expert and rows
+// [m0, mlim).  Every wave finds it by itself: lane l counts the tiles of experts
+// l*per .. of the offsets, a prefix sum over the lanes and a ballot give the
+// lane that holds tile i, and that lane's registers the rest.  The offsets are
+// loaded all at once; this takes about 1 us and saves the launch that would
+// build a table.  Offsets are cut to [0, rows] so that no index leaves c.
+// False when i is no tile.
+__device__ __forceinline__ bool find_tile(const Mx4Args& a, int lane, int i, int& e, int& m0, int& mlim) {
+  constexpr int BM = 16;
   if (a.offsets == nullptr) {
-    if (i >= (a.rows + bm - 1) / bm) return false;
+    if (i >= (a.rows + BM - 1) / BM) return false;
     e = 0;
-    m0 = i * bm;
+    m0 = i * BM;
     mlim = a.rows;
     return true;
   }
-  const int per = (a.E + 63) / 64;   // <= 8
-  int cnt[8], sum = 0;
-  const int e0 = lane * per;
-  int o = min(max(a.offsets[min(e0, a.E)], 0), a.rows);
+  constexpr int PER = 8;             // experts a lane at most
+  const int per = (a.E + 63) / 64, e0 = lane * per;
+  int o[PER + 1], cnt[PER], sum = 0;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    cnt[q] = 0;
-    if (q < per) {
-      const int o1 = min(max(a.offsets[min(e0 + q + 1, a.E)], 0), a.rows);
-      cnt[q] = max(0, o1 - o + bm - 1) / bm;
-      o = o1;
-    }
+  for (int q = 0; q <= PER; ++q) {
+    o[q] = 0;
+    if (q <= per) o[q] = a.offsets[min(e0 + q, a.E)];
+  }
+#pragma unroll
+  for (int q = 0; q <= PER; ++q) o[q] = min(max(o[q], 0), a.rows);
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    cnt[q] = q < per ? max(0, o[q + 1] - o[q] + BM - 1) / BM : 0;
     sum += cnt[q];
   }
-  int inc = sum;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int v = __shfl_up(inc, off);
-    if (lane >= off) inc += v;
-  }
+  int inc = sum;   // inclusive prefix sum over the lanes: within rows of 16, then over the rows
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x112, 0xF, 0xF, false);
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x114, 0xF, 0xF, false);
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x118, 0xF, 0xF, false);
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x142, 0xA, 0xF, false);   // row_bcast 15 into rows 1 and 3
+  inc += __builtin_amdgcn_update_dpp(0, inc, 0x143, 0xC, 0xF, false);   // row_bcast 31 into rows 2 and 3
   const uint64_t hit = __ballot(inc > i);
   if (hit == 0) return false;
   const int src = __builtin_ctzll(hit);
   int local = i - __builtin_amdgcn_readlane(inc - sum, src);
-  int q = 0;
+  int q = 0, first = __builtin_amdgcn_readlane(o[0], src), last = __builtin_amdgcn_readlane(o[1], src);
 #pragma unroll
-  for (int u = 0; u < 7; ++u) {
+  for (int u = 0; u < PER - 1; ++u) {
     const int c = __builtin_amdgcn_readlane(cnt[u], src);
     if (q == u && local >= c) {
       local -= c;
       q = u + 1;
+      first = __builtin_amdgcn_readlane(o[u + 1], src);
+      last = __builtin_amdgcn_readlane(o[u + 2], src);
     }
   }
   e = src * per + q;
-  const int first = min(max(a.offsets[e], 0), a.rows);
-  m0 = first + local * bm;
-  mlim = min(max(a.offsets[e + 1], 0), a.rows);
+  m0 = first + local * BM;
+  mlim = last;
   return true;
 }
 
 // f / row_div by the multiplier and shift the host chose (f < 2^31; exact)
 __device__ __forceinline__ int div_by(uint32_t f, uint32_t mul, int shift) { return (int)(((uint64_t)f * mul) >> shift); }
 
-// A's row of row r of c, or -1 (reads as zeros)
-__device__ __forceinline__ int a_row(const Mx4Args& a, int r) {
-  int s = r;
-  if (a.row_map) {
-    const int f = a.row_map[r];
-    s = f < 0 ? -1 : div_by((uint32_t)f, a.div_mul, a.div_shift);
-  }
+// A's row for entry f of the row map (for row f of c without one), or -1 (reads as zeros)
+__device__ __forceinline__ int a_row(const Mx4Args& a, int f) {
+  const int s = a.row_map == nullptr ? f : f < 0 ? -1 : div_by((uint32_t)f, a.div_mul, a.div_shift);
   return (uint32_t)s < (uint32_t)a.a_rows ? s : -1;
 }
 
@@ -133,16 +134,14 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
   const int g = lane >> 4, rl = lane & 15;
   const int tile = blockIdx.x / n_groups, n0 = blockIdx.x % n_groups * (16 * CF);
   int e, m0, mlim;
-  if (!find_tile(a, 16, lane, tile, e, m0, mlim)) return;
+  if (!find_tile(a, lane, tile, e, m0, mlim)) return;
   const uint32_t pb = (uint32_t)a.KB * 16, pa = FP8 ? (uint32_t)a.K : pb;   // code bytes of a row
   const auto rb = make_rsrc(a.b + (size_t)e * a.N * pb, (uint32_t)a.N * pb);
   const auto rsb = make_rsrc(a.sb + (size_t)e * a.N * a.KB, (uint32_t)a.N * a.KB);
   const auto ra = make_rsrc(a.a, (uint32_t)a.a_rows * pa);
   const auto rsa = make_rsrc(a.sa, (uint32_t)a.a_rows * a.KB);
   const int m = m0 + rl;
-  const int row = m < mlim ? a_row(a, m) : -1;
-  const bool mok = row >= 0;
-  const uint32_t oa = mok ? (uint32_t)row * pa : 0, osa = mok ? (uint32_t)row * a.KB : 0;
+  const int entry = m >= mlim ? -1 : a.row_map ? a.row_map[m] : m;   // (used below the weights' loads: they go first)
   f32x4_t acc[CF];
 #pragma unroll
   for (int c = 0; c < CF; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -168,6 +167,10 @@ __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups
         sb[c][u] = scale(rsb, (uint32_t)n * a.KB, in, kt);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    const int row = entry < 0 ? -1 : a_row(a, entry);
+    const bool mok = row >= 0;
+    const uint32_t oa = mok ? (uint32_t)row * pa : 0, osa = mok ? (uint32_t)row * a.KB : 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kt = kt0 + u;
