@@ -128,7 +128,9 @@ __device__ __forceinline__ void store4(const Mx4Args& a, int m, int n, f32x4_t v
 template <bool FP8, bool SC4, int CF>
 __global__ __launch_bounds__(256) void mx4_stream_kernel(Mx4Args a, int n_groups) {
   constexpr int NW = 4;
-  constexpr int U = 4;                         // K steps whose loads are in flight together
+  // K steps whose loads are in flight together; of a short K more would be steps that are not there (64 tokens at 2048
+  // x 768: 12.2 us with 4, 10.4 with 2)
+  constexpr int U = CF == 4 ? 2 : 4;
   __shared__ f32x4_t s_acc[NW][CF][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, rl = lane & 15;
