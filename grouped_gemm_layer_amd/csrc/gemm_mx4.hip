@@ -845,34 +845,35 @@ hipError_t launch_tiles(const Mx4Args& a, hipStream_t s) {
                        n_tiles);
 }
 
-// What the stream kernel and the 128 x 128 tiles take, in us, as fitted to some 100 sizes (1 to 8192 rows, 1 to 128
-// experts, N 256 to 4096, K 128 to 4096): good to 30 %.  The choice they gave was the better one, or within 4 % of it,
-// but for 3 of them (10, 14 and 29 %).
+// What the stream kernel and the 128 x 128 tiles take, in us, as fitted to 107 sizes (1 to 8192 rows, 1 to 128 experts,
+// N 256 to 4096, K 128 to 4480): good to 20 %, and the choice they give was within 4 % of the better one but for two of
+// the sizes (9 and 11 %).
 //
-// The stream kernel reads the weights once for every 16 rows of an expert, which costs most where all 16 are there (and
-// about 200 of K more for what a block does besides).  Tiles come in rounds of two on every compute unit, each as long
-// as K and a little more.  Both measured, stream and tiles: 32 rows on 32 of 128 experts, 1536 x 2048: 13.4 and 17.5;
-// 64 rows on 56: 18.5 and 18.0, 128 rows on 81: 27.6 and 25.9; 64 rows of one 4096 x 4096 weight 13.6 and 16.9, 128
-// rows 24.1 and 16.6; 2048 rows of one 1024 x 256 weight 11.4 and 8.4, 512 rows of 64 4096 x 128 ones 15.5 and 18.8.
+// The stream kernel reads the weights once for every 16 rows of an expert, which costs most where all 16 are there.
+// Tiles come in rounds of two on every compute unit, each as long as K and a little more.  Both measured, stream and
+// tiles: 32 rows on 32 of 128 experts, 1536 x 2048: 13.2 and 17.6; 64 rows on 56: 20.3 and 18.6, 128 rows on 81: 28.7 and
+// 25.9; 64 rows of one 4096 x 4096 weight 13.2 and 17.0, 128 rows 24.1 and 16.8; 2048 rows of one 1024 x 256 weight 11.4
+// and 8.4, 512 rows of 64 4096 x 128 ones 10.1 and 18.7.
+bool few_k(const Mx4Args& a) { return a.K <= 3 * 4 * KSTEP; }   // up to 3 steps for each wave of the stream kernel
 double stream_us(const Mx4Args& a) {
   const double tiles = (double)max_tiles(a, 16), fill = a.rows / (16 * tiles);
-  return 4 + 0.29 * (0.4 + 0.6 * fill) * tiles * a.N * (a.K + 200.0) / 2 / (1 << 20);
+  return 6 + (few_k(a) ? 0.2 : 0.28) * (0.4 + 0.6 * fill) * tiles * a.N * (a.K + 60.0) / 2 / (1 << 20);
 }
 double tile_us(const Mx4Args& a) {
   const double tiles = (double)max_tiles(a, 128) * ((a.N + 127) / 128), rounds = tiles / resident_blocks(2);
   const int stage = a.a_fp8 ? 128 : 256, stages = (a.K + stage - 1) / stage;
-  return 6 + (rounds < 1 ? 1 : rounds) * (1.6 + 0.75 * (stages < 2 ? 2 : stages));
+  return 6 + (rounds < 1 ? 1 : rounds) * (2 + 0.8 * (stages < 2 ? 2 : stages));
 }
 
-// Four fragments of columns to a wave of the stream kernel read A less often, two have more blocks: with up to 3 K steps
-// a wave 64 tokens on 48 experts' 1000 x 1120 took 9.1 and 10.0 us, 16 tokens on 8 experts' 4096 x 1536 9.0 and 10.1;
+// Four fragments of columns to a wave of the stream kernel read A less often, two have more blocks: with a short K 64
+// tokens on 48 experts' 1000 x 1120 took 9.1 and 10.0 us, 16 tokens on 8 experts' 4096 x 1536 9.0 and 10.1;
 // with 4 the 32 rows above 15.1 and 13.4.  (One fragment: 16.3.)
 template <bool FP8, bool SC4>
 hipError_t launch_formats(const Mx4Args& a, hipStream_t s) {
   // scales that pass through registers are read 8 bytes at a time: that many in each array
   const bool room = SC4 || ((int64_t)a.a_rows * a.KB >= 8 && (int64_t)a.E * a.N * a.KB >= 8);
   if (!room || stream_us(a) <= tile_us(a))
-    return a.K <= 3 * 4 * KSTEP ? launch_stream<FP8, SC4, 4>(a, s) : launch_stream<FP8, SC4, 2>(a, s);
+    return few_k(a) ? launch_stream<FP8, SC4, 4>(a, s) : launch_stream<FP8, SC4, 2>(a, s);
   if constexpr (SC4) {
     // 256 x 256 tiles halve the operands' traffic and want few partial tiles, one for every compute unit and a K that
     // outweighs the walk from tile to tile.  Against 128 x 128 ones: 1024 rows for each of 128 experts, 1536 x 2048:

@@ -225,11 +225,11 @@ CASES = [
 # long enough for the tiles through LDS: 128 x 128, then 256 x 256; K of whole and of broken steps, words and stages
 TILED = [
     ([3000, 5100], 4200, 40, None, 1),
-    ([100] * 300 + [0] * 212, 360, 160, 64, 4),
+    ([100] * 400 + [0] * 112, 360, 160, 64, 4),
     ([140, 900, 0, 12, 329], 1336, 1120, 100, 6),
     ([130, 0, 5, 64, 2700], 1500, 512, 50, 4),
     ([1000, 24, 1], 1230, 1664, None, 1),
-    ([28] * 10, 2451, 2048, 12, 7),
+    ([30] * 10, 2451, 2048, 12, 7),
     ([257, 1], 3601, 2080, None, 1),
     ([1700, 1, 2500], 4100, 2048, 700, 3),
     ([4111], 4099, 2170, None, 1),
