@@ -12,6 +12,8 @@
 #include "gemm_common.h"
 #include "row_vec.h"
 
+#include <algorithm>
+
 namespace moe {
 namespace {
 
@@ -824,7 +826,7 @@ void mx4_tile_kernel(Mx4Args a, int n_tiles) {
 
 // row tiles of height bm at most: every expert with rows ends in a partial one
 int64_t max_tiles(const Mx4Args& a, int bm) {
-  if (a.offsets == nullptr) return ((int64_t)a.rows + bm - 1) / bm;
+  if (a.offsets == nullptr || a.E == 1) return ((int64_t)a.rows + bm - 1) / bm;
   return (a.E < a.rows ? a.E : a.rows) + (int64_t)a.rows / bm;
 }
 
@@ -865,6 +867,19 @@ double tile_us(const Mx4Args& a) {
   return 6 + (rounds < 1 ? 1 : rounds) * (2 + 0.8 * (stages < 2 ? 2 : stages));
 }
 
+// 256 x 256 tiles halve the operands' traffic: a round of one on every compute unit takes 1.2 times (K = 4096) to
+// 1.45 times (short K) a round of two 128 x 128 tiles there and does twice the work, but more of it is partial tiles and
+// the last round's idle units.  Of 40 sizes with 256 rows an expert and more the rule was right or within 8 %.  Large and small
+// measured: 1024 rows for each of 128 experts, 1536 x 2048, 275 us and 324, 512 rows 185 and 207, 256 rows 118 and 112;
+// 512 rows of 4096 x 1536 393 and 448; one 4096 x 4096 weight, 4096 rows 44 and 57, 2048 rows 38 and 33; 512 rows of 16
+// 2048 x 1024 weights 29 and 25.
+bool big_tiles(const Mx4Args& a) {
+  const int64_t units = resident_blocks(1), big = (max_tiles(a, 256) * ((a.N + 255) / 256) + units - 1) / units;
+  const double experts = a.E == 1 ? 0 : a.E < a.rows ? a.E : a.rows;
+  const double small = (a.rows / 128.0 + experts / 2) * ((a.N + 127) / 128) / (2 * units);
+  return std::min(1.45, 1.1 + 400.0 / a.K) * big < small;
+}
+
 // Four fragments of columns to a wave of the stream kernel read A less often, two have more blocks: with a short K 64
 // tokens on 48 experts' 1000 x 1120 took 9.1 and 10.0 us, 16 tokens on 8 experts' 4096 x 1536 9.0 and 10.1;
 // with 4 the 32 rows above 15.1 and 13.4.  (One fragment: 16.3.)
@@ -874,15 +889,8 @@ hipError_t launch_formats(const Mx4Args& a, hipStream_t s) {
   const bool room = SC4 || ((int64_t)a.a_rows * a.KB >= 8 && (int64_t)a.E * a.N * a.KB >= 8);
   if (!room || stream_us(a) <= tile_us(a))
     return few_k(a) ? launch_stream<FP8, SC4, 4>(a, s) : launch_stream<FP8, SC4, 2>(a, s);
-  if constexpr (SC4) {
-    // 256 x 256 tiles halve the operands' traffic and want few partial tiles, one for every compute unit and a K that
-    // outweighs the walk from tile to tile.  Against 128 x 128 ones: 1024 rows for each of 128 experts, 1536 x 2048:
-    // 302 us and 324 (MXFP8 436, 471), 4096 rows of one 4096 x 4096 weight 44 and 57; but for 512 rows each 177 and
-    // 173, for 256 rows 139 and 105, for 2048 rows of the one weight 39 and 33, for 1024 rows each at K = 768 209 and 205.
-    const int64_t tiles = (int64_t)(a.rows / 256) * ((a.N + 255) / 256);
-    if (a.rows / a.E >= 1024 && a.K >= 2048 && tiles >= resident_blocks(1))
-      return launch_tiles<Mx4Cfg<FP8, SC4, 256, 256, 2, 4, 1>>(a, s);
-  }
+  if constexpr (SC4)
+    if (big_tiles(a)) return launch_tiles<Mx4Cfg<FP8, SC4, 256, 256, 2, 4, 1>>(a, s);
   return launch_tiles<Mx4Cfg<FP8, SC4, 128, 128, 2, 2, 2>>(a, s);
 }
 

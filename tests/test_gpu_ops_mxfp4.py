@@ -231,8 +231,8 @@ TILED = [
     ([1000, 24, 1], 1230, 1664, None, 1),
     ([30] * 10, 2451, 2048, 12, 7),
     ([257, 1], 3601, 2080, None, 1),
-    ([1700, 1, 2500], 4100, 2048, 700, 3),
-    ([4111], 4099, 2170, None, 1),
+    ([1700, 1, 5000], 4100, 1152, 700, 3),
+    ([4090], 4090, 2170, None, 1),
 ]
 
 
@@ -278,7 +278,7 @@ def test_product(case, fmt, typ):
 
 
 @pytest.mark.parametrize("rows,N,K", [(1, 200, 384), (16, 200, 384), (200, 200, 384), (900, 200, 384),
-                                      (1500, 3800, 384), (4100, 4100, 2048)])
+                                      (1500, 3800, 384), (4090, 4090, 1024)])
 def test_product_without_experts(rows, N, K):
     import torch
     import grouped_gemm_layer_amd as g
@@ -289,7 +289,7 @@ def test_product_without_experts(rows, N, K):
 
 
 @pytest.mark.parametrize("counts,N,K", [([3, 0, 5], 72, 256), ([100, 70, 0], 72, 256), ([600, 300], 72, 256),
-                                        ([100, 1900, 0], 1100, 1024), ([2500, 2000], 4100, 2048)])
+                                        ([100, 1900, 0], 1100, 1024), ([4000, 2700], 4100, 1024)])
 def test_rows_behind_the_last_stay(counts, N, K):
     """c longer than the rows routed: the rest is left as it was; no rows at all; offsets past c are cut."""
     import torch
@@ -310,7 +310,7 @@ def test_rows_behind_the_last_stay(counts, N, K):
     assert torch.equal(buf[p.rows:], torch.full_like(buf[p.rows:], 5.0))
 
 
-@pytest.mark.parametrize("rows,N,K", [(8, 90, 352), (100, 90, 352), (400, 90, 352), (1600, 1100, 1056), (2100, 4100, 2048)])
+@pytest.mark.parametrize("rows,N,K", [(8, 90, 352), (100, 90, 352), (400, 90, 352), (1600, 1100, 1056), (3300, 4100, 1024)])
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 def test_scale_255_makes_what_it_enters_nan(fmt, rows, N, K):
     import torch
@@ -374,7 +374,7 @@ def test_large_output_offsets():
 
 
 @pytest.mark.parametrize("counts,N,K", [([3, 0, 5], 136, 512), ([100, 70, 0, 40], 136, 512), ([300, 600], 136, 512),
-                                        ([300, 1600], 1136, 1024), ([2200, 2000], 4100, 2048)])
+                                        ([300, 1600], 1136, 1024), ([4000, 2700], 4100, 1024)])
 def test_graph_replays_and_streams(counts, N, K):
     import torch
     import grouped_gemm_layer_amd as g
